@@ -57,7 +57,7 @@ typedef enum {
   MOE_ERR_DEVICE_RANGE = 6    /* a device kernel met an out-of-range expert id */
 } moe_status_t;
 
-typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP8_E4M3 = 1 } moe_dtype_t;
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP8_E4M3 = 1, MOE_DT_FP32 = 2 } moe_dtype_t;
 
 /*
  * Router (token routing, page Introduction).
@@ -291,6 +291,74 @@ size_t moe_fused_h_amax_offset(void);
 moe_status_t moe_fused_forward_timed(const moe_fused_args* args, void* workspace,
                                      size_t workspace_bytes, moe_stream_t stream,
                                      void* const* events, int n_events);
+
+/*
+ * 4-bit weights with group scales.  A weight tensor [rows, K] stands for
+ *   value[r][k] = scale[r][k / group] * (code[r][k] - zero[r][k / group]),
+ * code in 0..15, the last group of a row short when K % group != 0.  The pages
+ * stop at 8 bits; decode reads every touched expert's weights once per call, so
+ * the halved codes halve what it is bound by.
+ *   codes   uint8 [rows, K/2]               even k in the low nibble, 16-byte aligned
+ *   scales  [rows, ceil(K / group)]         fp32 or bf16 (scale_dtype)
+ *   zeros   uint8 [rows, ceil(K / group)]   each in 0..15; NULL: 8 everywhere
+ *   group   32, 64 or 128
+ * K % 32 == 0 (rows of codes start on 16 bytes).
+ */
+typedef struct {
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  moe_dtype_t scale_dtype; /* MOE_DT_FP32 or MOE_DT_BF16 */
+  int group;
+} moe_w4_tensor;
+
+/*
+ * Matrix-vector products with 4-bit weights, for a few tokens:
+ *   out[t][n] = sum_k x[t][k] * value[n][k],
+ * products exact, sums in fp32, one rounding when out is bf16.
+ *   x    bf16 [T, K]
+ *   w    [N, K] (not NULL)
+ *   out  bf16 or fp32 [T, N] (out_dtype)
+ * Requires T >= 0 (0 enqueues nothing), N >= 1, K >= 32, K % 32 == 0
+ * (MOE_ERR_UNSUPPORTED otherwise), T*K and T*N < 2^31 (MOE_ERR_UNSUPPORTED).
+ * Results do not depend on anything but the arguments (no atomics).
+ */
+moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tensor* w, void* out,
+                           moe_dtype_t out_dtype, moe_stream_t stream);
+
+/* Arguments of the MoE layer with 4-bit experts. */
+typedef struct {
+  const void* x;              /* bf16 [T, H] */
+  const float* router_logits; /* fp32 [T, E], finite */
+  moe_w4_tensor w13;          /* [E * 2I, H]: per expert gate rows then up rows */
+  moe_w4_tensor w2;           /* [E * H, I] */
+  int T, H, I, E, top_k, renormalize;
+  void* out;                  /* bf16 [T, H] */
+  int32_t* topk_ids_out;      /* optional int32 [T, top_k] */
+  float* topk_w_out;          /* optional fp32 [T, top_k] */
+  int32_t* counts_out;        /* optional int32 [E] */
+} moe_w4_args;
+
+/* Workspace bytes moe_w4_forward needs for these sizes (0 if invalid). */
+size_t moe_w4_workspace_size(int T, int H, int I, int E, int top_k);
+
+/* Kernels one moe_w4_forward call with these sizes launches (0 for T = 0, -1 if
+ * the sizes are invalid or unsupported).  Host only. */
+int moe_w4_launch_count(int T, int H, int I, int E, int top_k);
+
+/*
+ * The MoE layer of moe_fused_forward with 4-bit expert weights, for a few
+ * tokens: the same router, h = SiLU(gate) * up and combine; no activation
+ * quantisation.  Any T works; it is built for decode batches, where reading
+ * the touched experts' codes bounds the call.
+ * Requires 1 <= top_k <= E <= 1024, H % 32 == 0 and I % 32 == 0
+ * (MOE_ERR_UNSUPPORTED otherwise), T >= 0, a device of compute capability
+ * 10.3, workspace of moe_w4_workspace_size() bytes (256-byte aligned) that no
+ * other in-flight call uses.  T == 0 returns MOE_OK and enqueues nothing (no
+ * output is written).  Results do not depend on anything but the arguments.
+ */
+moe_status_t moe_w4_forward(const moe_w4_args* args, void* workspace, size_t workspace_bytes,
+                            moe_stream_t stream);
 
 /* Synchronises `stream`, reads the status word that the last call using
  * `workspace` left there, and returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT or

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
 MOE_OK = 0
 MOE_DT_BF16 = 0
 MOE_DT_FP8_E4M3 = 1
+MOE_DT_FP32 = 2
 MOE_DEBUG_FORCE_TIMEOUT = 0x1
 MOE_DEBUG_TRACE = 0x2
 MOE_FLAG_TOKENS_IN_M = 0x4   # both GEMMs: tokens in the MMA M slot (ablation of the swap)
@@ -66,6 +67,35 @@ class MoeFusedArgs(ctypes.Structure):
     ]
 
 
+class MoeW4Tensor(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+        ("scale_dtype", ctypes.c_int),
+        ("group", ctypes.c_int),
+    ]
+
+
+class MoeW4Args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("router_logits", ctypes.c_void_p),
+        ("w13", MoeW4Tensor),
+        ("w2", MoeW4Tensor),
+        ("T", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("I", ctypes.c_int),
+        ("E", ctypes.c_int),
+        ("top_k", ctypes.c_int),
+        ("renormalize", ctypes.c_int),
+        ("out", ctypes.c_void_p),
+        ("topk_ids_out", ctypes.c_void_p),
+        ("topk_w_out", ctypes.c_void_p),
+        ("counts_out", ctypes.c_void_p),
+    ]
+
+
 def load():
     """Load libmoe_gb300.so (raises if it has not been built)."""
     global _lib
@@ -100,6 +130,14 @@ def load():
         L.moe_fused_forward_down.argtypes = [ctypes.POINTER(MoeFusedArgs), P, sz, P]
         L.moe_fused_h_amax_offset.argtypes = []
         L.moe_fused_h_amax_offset.restype = sz
+        L.moe_w4_matvec.argtypes = [P, i, i, i, ctypes.POINTER(MoeW4Tensor), P, i, P]
+        L.moe_w4_matvec.restype = i
+        L.moe_w4_workspace_size.argtypes = [i, i, i, i, i]
+        L.moe_w4_workspace_size.restype = sz
+        L.moe_w4_launch_count.argtypes = [i, i, i, i, i]
+        L.moe_w4_launch_count.restype = i
+        L.moe_w4_forward.argtypes = [ctypes.POINTER(MoeW4Args), P, sz, P]
+        L.moe_w4_forward.restype = i
         L.moe_check_status.argtypes = [P, P]
         L.moe_status_string.argtypes = [i]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -402,6 +440,129 @@ def read_trace(workspace, T, H, I, E, top_k, dtype):
     return raw.view(torch.int64).reshape(2, TRACE_MAX_CTAS, 4)
 
 
+class W4Tensor:
+    """A weight tensor [.., N, K] held in 4 bits (include/moe_gb300.h):
+
+        value = scale[.., n, k // group] * (code[.., n, k] - zero[.., n, k // group])
+
+    codes: uint8 [.., N, K/2], even k in the low nibble; scales: fp32 or bf16
+    [.., N, ceil(K / group)]; zeros: uint8 of the scales' shape, each in 0..15, or
+    None (8 everywhere); group: 32, 64 or 128.  The tensors are checked once here
+    and kept; calls use them in place, so they are not to be resized or moved.
+    """
+
+    __slots__ = ("codes", "scales", "zeros", "group", "shape", "device", "_c")
+
+    def __init__(self, codes, scales, zeros=None, group: int = 128):
+        import torch
+        if group not in (32, 64, 128):
+            raise ValueError(f"group must be 32, 64 or 128, got {group}")
+        if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.float32,
+                                                                        torch.bfloat16):
+            raise ValueError("scales must be a float32 or bfloat16 tensor")
+        _require(codes, torch.uint8, "codes")
+        if codes.dim() < 2:
+            raise ValueError(f"codes must be [.., N, K/2], got {tuple(codes.shape)}")
+        K = 2 * codes.shape[-1]
+        groups = tuple(codes.shape[:-1]) + (-(-K // group),)
+        _require(scales, scales.dtype, "scales", groups)
+        if zeros is not None:
+            _require(zeros, torch.uint8, "zeros", groups)
+        self.codes, self.scales, self.zeros, self.group = codes, scales, zeros, group
+        self.shape = tuple(codes.shape[:-1]) + (K,)
+        self.device = codes.device
+        self._c = MoeW4Tensor(codes.data_ptr(), scales.data_ptr(),
+                              None if zeros is None else zeros.data_ptr(),
+                              MOE_DT_FP32 if scales.dtype == torch.float32 else MOE_DT_BF16, group)
+
+
+def moe_w4_matvec(x, w: W4Tensor, out=None, out_dtype=None, stream=None):
+    """Matrix-vector products with 4-bit weights, for a few tokens: out = x w^T.
+    x: bf16 [T, K]; w: W4Tensor [N, K]; out: bf16 or fp32 [T, N] (allocated, of
+    `out_dtype`, bf16 by default, when not given).  Returns out."""
+    import torch
+    _require(x, torch.bfloat16, "x")
+    if len(w.shape) != 2 or x.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} does not fit a weight of shape {w.shape}")
+    T, (N, K) = x.shape[0], w.shape
+    if out is None:
+        out = torch.empty(T, N, dtype=out_dtype or torch.bfloat16, device=x.device)
+        if stream is not None:
+            out.record_stream(stream)
+    if out.dtype not in (torch.bfloat16, torch.float32) or out_dtype not in (None, out.dtype):
+        raise ValueError(f"out must be bfloat16 or float32 (out_dtype {out_dtype}), got {out.dtype}")
+    _require(out, out.dtype, "out", (T, N))
+    _check(load().moe_w4_matvec(_ptr(x), T, K, N, ctypes.byref(w._c), _ptr(out),
+                                MOE_DT_FP32 if out.dtype == torch.float32 else MOE_DT_BF16,
+                                _stream(stream)), "moe_w4_matvec")
+    return out
+
+
+def moe_w4_workspace_size(T: int, H: int, I: int, E: int, top_k: int) -> int:
+    return int(load().moe_w4_workspace_size(T, H, I, E, top_k))
+
+
+def moe_w4_launch_count(T: int, H: int, I: int, E: int, top_k: int) -> int:
+    """Kernels one moe_w4_forward call launches (-1: invalid sizes)."""
+    return int(load().moe_w4_launch_count(T, H, I, E, top_k))
+
+
+def alloc_w4_workspace(T, H, I, E, top_k, device="cuda"):
+    import torch
+    n = moe_w4_workspace_size(T, H, I, E, top_k)
+    if n == 0:
+        raise MoeError(1, "moe_w4_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_w4_forward(x, router_logits, w13: W4Tensor, w2: W4Tensor, top_k: int,
+                   renormalize: bool = True, out=None, workspace=None, topk_ids_out=None,
+                   topk_w_out=None, counts_out=None, stream=None):
+    """MoE layer with 4-bit experts, for a few tokens (see include/moe_gb300.h).
+
+    x bf16 [T, H]; router_logits fp32 [T, E]; w13: W4Tensor [E, 2I, H] (gate rows,
+    then up rows); w2: W4Tensor [E, H, I].  Returns out bf16 [T, H].  A workspace
+    (alloc_w4_workspace) serves one call in flight; without one, it is allocated
+    for this call.
+    """
+    import torch
+    _require(x, torch.bfloat16, "x")
+    _require(router_logits, torch.float32, "router_logits")
+    if x.dim() != 2 or router_logits.dim() != 2 or router_logits.shape[0] != x.shape[0]:
+        raise ValueError("x must be [T, H] and router_logits [T, E]")
+    T, H = x.shape
+    E = router_logits.shape[1]
+    if len(w13.shape) != 3 or w13.shape[0] != E or w13.shape[2] != H or w13.shape[1] % 2:
+        raise ValueError(f"w13 must be [E, 2I, H] = [{E}, 2I, {H}], got {w13.shape}")
+    I = w13.shape[1] // 2
+    if w2.shape != (E, H, I):
+        raise ValueError(f"w2 must be [E, H, I] = [{E}, {H}, {I}], got {w2.shape}")
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        if stream is not None:
+            out.record_stream(stream)
+    _require(out, torch.bfloat16, "out", (T, H))
+    if topk_ids_out is not None:
+        _require(topk_ids_out, torch.int32, "topk_ids_out", (T, top_k))
+    if topk_w_out is not None:
+        _require(topk_w_out, torch.float32, "topk_w_out", (T, top_k))
+    if counts_out is not None:
+        _require(counts_out, torch.int32, "counts_out", (E,))
+    if workspace is None:
+        workspace = alloc_w4_workspace(T, H, I, E, top_k, x.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    _require(workspace, torch.uint8, "workspace")
+    args = MoeW4Args(x.data_ptr(), router_logits.data_ptr(), w13._c, w2._c, T, H, I, E, top_k,
+                     int(bool(renormalize)), out.data_ptr(),
+                     None if topk_ids_out is None else topk_ids_out.data_ptr(),
+                     None if topk_w_out is None else topk_w_out.data_ptr(),
+                     None if counts_out is None else counts_out.data_ptr())
+    _check(load().moe_w4_forward(ctypes.byref(args), _ptr(workspace), workspace.numel(),
+                                 _stream(stream)), "moe_w4_forward")
+    return out
+
+
 def moe_check_status(workspace, stream=None) -> int:
     """Synchronise and return the status the last call left in the workspace (0 = MOE_OK)."""
     return int(load().moe_check_status(_ptr(workspace), _stream(stream)))
@@ -413,4 +574,6 @@ __all__ = ["load", "moe_fused_forward_gate_up", "moe_fused_forward_down", "h_ama
            "moe_inv_rope_quant_per_head", "moe_fused_forward", "moe_check_status", "alloc_workspace",
            "status_string", "MoeError", "make_step_events", "MoeFusedArgs", "MOE_DT_BF16", "MOE_DT_FP8_E4M3",
            "MOE_DEBUG_FORCE_TIMEOUT", "MOE_FLAG_TOKENS_IN_M",
-           "MOE_FLAG_WEIGHTS_IN_M", "MOE_FLAG_NO_SM_PAIRS", "MOE_FLAG_ONE_KERNEL", "LIB_PATH"]
+           "MOE_FLAG_WEIGHTS_IN_M", "MOE_FLAG_NO_SM_PAIRS", "MOE_FLAG_ONE_KERNEL", "LIB_PATH",
+           "W4Tensor", "moe_w4_matvec", "moe_w4_forward", "moe_w4_workspace_size",
+           "moe_w4_launch_count", "alloc_w4_workspace", "MOE_DT_FP32"]

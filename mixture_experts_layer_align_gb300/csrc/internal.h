@@ -166,6 +166,29 @@ cudaError_t launch_inv_rope_quant(const __nv_bfloat16* x, const int32_t* pos, co
                                   uint8_t* codes, float* scales, Ctrl* ctrl, float* partials,
                                   int num_sms, cudaStream_t st);
 
+// ------------------------------------------------------------ 4-bit weights
+struct W4View {
+  const uint8_t* codes;  // [rows][K/2], even k in the low nibble
+  const void* scales;    // [rows][ceil(K/group)] fp32 or bf16
+  const uint8_t* zeros;  // same shape, or null: 8
+  int scale_bf16;
+  int group;             // 32, 64 or 128
+};
+constexpr int kW4Block = 8;  // tokens of one MMA column block: rows of an alignment block
+cudaError_t launch_w4_matvec(const __nv_bfloat16* x, int T, int K, int N, const W4View& w,
+                             void* out, bool out_fp32, cudaStream_t st);
+struct W4LayerParams {
+  const __nv_bfloat16* x;
+  W4View w13, w2;
+  int T, H, I, E, k;
+  int32_t* ids;  // [T*k] chosen experts
+  float* wts;    // [T*k] their router weights
+  float* h;      // [T*k][I]
+  __nv_bfloat16* out;
+};
+cudaError_t launch_w4_gate_up(const W4LayerParams& p, cudaStream_t st);
+cudaError_t launch_w4_down(const W4LayerParams& p, cudaStream_t st);
+
 // ------------------------------------------------------------ grouped GEMM
 struct GemmParams {
   // Row tiles {expert, first row, rows | (tiles of this expert << 12), index of

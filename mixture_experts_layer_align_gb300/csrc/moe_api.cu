@@ -701,6 +701,62 @@ moe_status_t fused_forward_impl(const moe_fused_args* a, void* workspace, size_t
   return MOE_OK;
 }
 
+// ------------------------------------------------------------ 4-bit weights
+W4View w4_view(const moe_w4_tensor& w) {
+  W4View v{};
+  v.codes = w.codes;
+  v.scales = w.scales;
+  v.zeros = w.zeros;
+  v.scale_bf16 = w.scale_dtype == MOE_DT_BF16 ? 1 : 0;
+  v.group = w.group;
+  return v;
+}
+
+// Format and, when the call reads the tensor, pointers.
+moe_status_t check_w4(const moe_w4_tensor& w, bool pointers) {
+  if (w.scale_dtype != MOE_DT_BF16 && w.scale_dtype != MOE_DT_FP32) return MOE_ERR_INVALID_ARG;
+  if (w.group != 32 && w.group != 64 && w.group != 128) return MOE_ERR_INVALID_ARG;
+  if (!pointers) return MOE_OK;
+  if (!w.codes || !w.scales || !aligned(w.codes, 16) ||
+      !aligned(w.scales, w.scale_dtype == MOE_DT_FP32 ? 4 : 2))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+bool w4_sizes_ok(int T, int H, int I, int E, int k) {
+  return T >= 0 && H >= 1 && I >= 1 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= E;
+}
+
+bool w4_sizes_supported(int T, int H, int I, int k) {
+  const long long P = static_cast<long long>(T) * k;
+  return H % 32 == 0 && I % 32 == 0 && P < (1ll << 31) / 2 && H < (1 << 19) && I < (1 << 18);
+}
+
+struct W4Layout {
+  size_t ctrl = 0, ids = 0, wts = 0, counts = 0, offsets = 0, sorted = 0, h = 0, total = 0;
+};
+
+W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
+  (void)H;
+  W4Layout L;
+  const size_t P = static_cast<size_t>(T) * k;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  L.ctrl = take(sizeof(Ctrl));
+  L.ids = take(sizeof(int32_t) * P);
+  L.wts = take(sizeof(float) * P);
+  L.counts = take(sizeof(int32_t) * E);
+  L.offsets = take(sizeof(int32_t) * (E + 1));
+  L.sorted = take(sizeof(int32_t) * (P + static_cast<size_t>(E) * (kW4Block - 1)));
+  L.h = take(sizeof(float) * P * I);
+  L.total = off;
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
@@ -755,6 +811,88 @@ moe_status_t moe_fused_forward_timed(const moe_fused_args* a, void* workspace,
     if (!events[i]) return MOE_ERR_INVALID_ARG;
   return fused_forward_impl(a, workspace, workspace_bytes, stream,
                             reinterpret_cast<cudaEvent_t const*>(events));
+}
+
+moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tensor* w, void* out,
+                           moe_dtype_t out_dtype, moe_stream_t stream) {
+  if (T < 0 || K < 1 || N < 1 || !w) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_FP32) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_w4(*w, T > 0);
+  if (st != MOE_OK) return st;
+  if (K % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * K >= (1ll << 31) || static_cast<long long>(T) * N >= (1ll << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !out || !aligned(x, 16) || !aligned(out, out_dtype == MOE_DT_FP32 ? 4 : 2))
+    return MOE_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = check_device(&dev);
+  if (st != MOE_OK) return st;
+  return launch_w4_matvec(static_cast<const __nv_bfloat16*>(x), T, K, N, w4_view(*w), out,
+                          out_dtype == MOE_DT_FP32, stream) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+size_t moe_w4_workspace_size(int T, int H, int I, int E, int top_k) {
+  if (!w4_sizes_ok(T, H, I, E, top_k)) return 0;
+  return make_w4_layout(T, H, I, E, top_k).total;
+}
+
+int moe_w4_launch_count(int T, int H, int I, int E, int top_k) {
+  if (!w4_sizes_ok(T, H, I, E, top_k) || !w4_sizes_supported(T, H, I, top_k)) return -1;
+  return T == 0 ? 0 : 4;  // router, alignment, gate/up, down
+}
+
+moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t workspace_bytes,
+                            moe_stream_t stream) {
+  if (!a) return MOE_ERR_INVALID_ARG;
+  const int T = a->T, H = a->H, I = a->I, E = a->E, k = a->top_k;
+  if (!w4_sizes_ok(T, H, I, E, k)) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_w4(a->w13, T > 0);
+  if (st == MOE_OK) st = check_w4(a->w2, T > 0);
+  if (st != MOE_OK) return st;
+  if (!w4_sizes_supported(T, H, I, k)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!a->x || !a->router_logits || !a->out || !aligned(a->x, 16) || !aligned(a->out, 16) ||
+      !aligned(a->router_logits, 4) || !aligned(a->topk_ids_out, 4) ||
+      !aligned(a->topk_w_out, 4) || !aligned(a->counts_out, 4))
+    return MOE_ERR_INVALID_ARG;
+  const W4Layout L = make_w4_layout(T, H, I, E, k);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  DeviceInfo dev;
+  st = check_device(&dev);
+  if (st != MOE_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  W4LayerParams p{};
+  p.x = static_cast<const __nv_bfloat16*>(a->x);
+  p.w13 = w4_view(a->w13);
+  p.w2 = w4_view(a->w2);
+  p.T = T;
+  p.H = H;
+  p.I = I;
+  p.E = E;
+  p.k = k;
+  p.ids = a->topk_ids_out ? a->topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
+  p.wts = a->topk_w_out ? a->topk_w_out : reinterpret_cast<float*>(ws + L.wts);
+  p.h = reinterpret_cast<float*>(ws + L.h);
+  p.out = static_cast<__nv_bfloat16*>(a->out);
+  if (launch_route_topk(a->router_logits, T, E, k, a->renormalize, p.ids, p.wts, nullptr, 0,
+                        nullptr, reinterpret_cast<Ctrl*>(ws + L.ctrl), nullptr, 0,
+                        stream) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  AlignParams ap{};
+  ap.ids = p.ids;
+  ap.P = T * k;
+  ap.E = E;
+  ap.bm = kW4Block;
+  ap.chunk = align_chunk();
+  ap.counts = a->counts_out ? a->counts_out : reinterpret_cast<int32_t*>(ws + L.counts);
+  ap.offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
+  ap.sorted_ids = reinterpret_cast<int32_t*>(ws + L.sorted);
+  if (launch_align(ap, stream) != cudaSuccess || launch_w4_gate_up(p, stream) != cudaSuccess || launch_w4_down(p, stream) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 moe_status_t moe_check_status(const void* workspace, moe_stream_t stream) {
