@@ -320,7 +320,8 @@ typedef struct {
  *   w    [N, K] (not NULL)
  *   out  bf16 or fp32 [T, N] (out_dtype)
  * Requires T >= 0 (0 enqueues nothing), N >= 1, K >= 32, K % 32 == 0
- * (MOE_ERR_UNSUPPORTED otherwise), T*K and T*N < 2^31 (MOE_ERR_UNSUPPORTED).
+ * (MOE_ERR_UNSUPPORTED otherwise), T < 2^20, T*K and T*N < 2^31
+ * (MOE_ERR_UNSUPPORTED).
  * Results do not depend on anything but the arguments (no atomics).
  */
 moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tensor* w, void* out,

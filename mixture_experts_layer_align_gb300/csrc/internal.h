@@ -174,20 +174,23 @@ struct W4View {
   int scale_bf16;
   int group;             // 32, 64 or 128
 };
-constexpr int kW4Block = 8;  // tokens of one MMA column block: rows of an alignment block
 cudaError_t launch_w4_matvec(const __nv_bfloat16* x, int T, int K, int N, const W4View& w,
                              void* out, bool out_fp32, cudaStream_t st);
 struct W4LayerParams {
   const __nv_bfloat16* x;
   W4View w13, w2;
   int T, H, I, E, k;
-  int32_t* ids;  // [T*k] chosen experts
-  float* wts;    // [T*k] their router weights
-  float* h;      // [T*k][I]
+  const float* wts;             // [T*k] router weights
+  const int32_t* sorted_ids;    // pair ids by expert in blocks of w4_block_rows(T), T*k pads
+  const int32_t* block_expert;  // expert of each block
+  const int32_t* num_padded;    // rows of all blocks
+  __nv_bfloat16* h;             // [T*k][I]
+  float* y;                     // [T*k][H]
   __nv_bfloat16* out;
 };
-cudaError_t launch_w4_gate_up(const W4LayerParams& p, cudaStream_t st);
-cudaError_t launch_w4_down(const W4LayerParams& p, cudaStream_t st);
+// Rows of an alignment block: the pairs of one expert that one thread block takes.
+int w4_block_rows(int T);
+cudaError_t launch_w4_layer(const W4LayerParams& p, cudaStream_t st);
 
 // ------------------------------------------------------------ grouped GEMM
 struct GemmParams {

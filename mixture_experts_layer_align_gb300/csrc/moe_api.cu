@@ -733,12 +733,13 @@ bool w4_sizes_supported(int T, int H, int I, int k) {
 }
 
 struct W4Layout {
-  size_t ctrl = 0, ids = 0, wts = 0, counts = 0, offsets = 0, sorted = 0, h = 0, total = 0;
+  size_t ctrl = 0, ids = 0, wts = 0, counts = 0, offsets = 0, sorted = 0, blocks = 0,
+         padded = 0, h = 0, y = 0, total = 0;
 };
 
 W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
-  (void)H;
   W4Layout L;
+  const int bm = w4_block_rows(T);
   const size_t P = static_cast<size_t>(T) * k;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -751,8 +752,12 @@ W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
   L.wts = take(sizeof(float) * P);
   L.counts = take(sizeof(int32_t) * E);
   L.offsets = take(sizeof(int32_t) * (E + 1));
-  L.sorted = take(sizeof(int32_t) * (P + static_cast<size_t>(E) * (kW4Block - 1)));
-  L.h = take(sizeof(float) * P * I);
+  const size_t rows = P + static_cast<size_t>(E) * (bm - 1);
+  L.sorted = take(sizeof(int32_t) * rows);
+  L.blocks = take(sizeof(int32_t) * (rows / bm));
+  L.padded = take(sizeof(int32_t));
+  L.h = take(sizeof(__nv_bfloat16) * P * I);
+  L.y = take(sizeof(float) * P * H);
   L.total = off;
   return L;
 }
@@ -820,7 +825,8 @@ moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tens
   moe_status_t st = check_w4(*w, T > 0);
   if (st != MOE_OK) return st;
   if (K % 32 != 0) return MOE_ERR_UNSUPPORTED;
-  if (static_cast<long long>(T) * K >= (1ll << 31) || static_cast<long long>(T) * N >= (1ll << 31))
+  if (T >= (1 << 20) || static_cast<long long>(T) * K >= (1ll << 31) ||
+      static_cast<long long>(T) * N >= (1ll << 31))
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !out || !aligned(x, 16) || !aligned(out, out_dtype == MOE_DT_FP32 ? 4 : 2))
@@ -841,7 +847,7 @@ size_t moe_w4_workspace_size(int T, int H, int I, int E, int top_k) {
 
 int moe_w4_launch_count(int T, int H, int I, int E, int top_k) {
   if (!w4_sizes_ok(T, H, I, E, top_k) || !w4_sizes_supported(T, H, I, top_k)) return -1;
-  return T == 0 ? 0 : 4;  // router, alignment, gate/up, down
+  return T == 0 ? 0 : 5;  // router, alignment, gate/up, down, combine
 }
 
 moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t workspace_bytes,
@@ -873,26 +879,31 @@ moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t worksp
   p.I = I;
   p.E = E;
   p.k = k;
-  p.ids = a->topk_ids_out ? a->topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
-  p.wts = a->topk_w_out ? a->topk_w_out : reinterpret_cast<float*>(ws + L.wts);
-  p.h = reinterpret_cast<float*>(ws + L.h);
-  p.out = static_cast<__nv_bfloat16*>(a->out);
-  if (launch_route_topk(a->router_logits, T, E, k, a->renormalize, p.ids, p.wts, nullptr, 0,
-                        nullptr, reinterpret_cast<Ctrl*>(ws + L.ctrl), nullptr, 0,
-                        stream) != cudaSuccess)
+  int32_t* ids = a->topk_ids_out ? a->topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
+  float* wts = a->topk_w_out ? a->topk_w_out : reinterpret_cast<float*>(ws + L.wts);
+  if (launch_route_topk(a->router_logits, T, E, k, a->renormalize, ids, wts, nullptr, 0, nullptr,
+                        reinterpret_cast<Ctrl*>(ws + L.ctrl), nullptr, 0, stream) != cudaSuccess)
     return MOE_ERR_CUDA;
   AlignParams ap{};
-  ap.ids = p.ids;
+  ap.ids = ids;
   ap.P = T * k;
   ap.E = E;
-  ap.bm = kW4Block;
+  ap.bm = w4_block_rows(T);
   ap.chunk = align_chunk();
   ap.counts = a->counts_out ? a->counts_out : reinterpret_cast<int32_t*>(ws + L.counts);
   ap.offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
   ap.sorted_ids = reinterpret_cast<int32_t*>(ws + L.sorted);
-  if (launch_align(ap, stream) != cudaSuccess || launch_w4_gate_up(p, stream) != cudaSuccess || launch_w4_down(p, stream) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  return MOE_OK;
+  ap.tile_expert = reinterpret_cast<int32_t*>(ws + L.blocks);
+  ap.num_padded = reinterpret_cast<int32_t*>(ws + L.padded);
+  if (launch_align(ap, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  p.wts = wts;
+  p.sorted_ids = ap.sorted_ids;
+  p.block_expert = ap.tile_expert;
+  p.num_padded = ap.num_padded;
+  p.h = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
+  p.y = reinterpret_cast<float*>(ws + L.y);
+  p.out = static_cast<__nv_bfloat16*>(a->out);
+  return launch_w4_layer(p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status_t moe_check_status(const void* workspace, moe_stream_t stream) {
