@@ -320,7 +320,7 @@ typedef struct {
  *   w    [N, K] (not NULL)
  *   out  bf16 or fp32 [T, N] (out_dtype)
  * Requires T >= 0 (0 enqueues nothing), N >= 1, K >= 32, K % 32 == 0
- * (MOE_ERR_UNSUPPORTED otherwise), T < 2^20, T*K and T*N < 2^31
+ * (MOE_ERR_UNSUPPORTED otherwise), T < 2^20, K <= 2^20, T*K and T*N < 2^31
  * (MOE_ERR_UNSUPPORTED).
  * Results do not depend on anything but the arguments (no atomics).
  */

@@ -825,7 +825,7 @@ moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tens
   moe_status_t st = check_w4(*w, T > 0);
   if (st != MOE_OK) return st;
   if (K % 32 != 0) return MOE_ERR_UNSUPPORTED;
-  if (T >= (1 << 20) || static_cast<long long>(T) * K >= (1ll << 31) ||
+  if (T >= (1 << 20) || K > (1 << 20) || static_cast<long long>(T) * K >= (1ll << 31) ||
       static_cast<long long>(T) * N >= (1ll << 31))
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;

@@ -45,8 +45,9 @@ def test_launch_count(lib):
     (dict(x=24), {}, 1), (dict(out=None), {}, 1), (dict(out=18), {}, 1),
     (dict(out=17, dtype=BF16), {}, 1), ({}, dict(codes=None), 1), ({}, dict(codes=8), 1),
     ({}, dict(scales=None), 1), ({}, dict(scales=18), 1), ({}, dict(group=0), 1),
-    ({}, dict(group=48), 1), ({}, dict(scale_dtype=FP8), 1), (dict(T=1 << 20, K=1 << 12), {}, 2),
-    (dict(T=1 << 20, N=1 << 12), {}, 2), (dict(T=0), {}, 0), (dict(T=0, x=None, out=None), {}, 0),
+    ({}, dict(group=48), 1), ({}, dict(scale_dtype=FP8), 1), (dict(T=1 << 20), {}, 2),
+    (dict(T=1 << 19, N=1 << 12), {}, 2), (dict(K=1 << 21), {}, 2),
+    (dict(T=1 << 13, K=1 << 18), {}, 2), (dict(T=0), {}, 0), (dict(T=0, x=None, out=None), {}, 0),
 ])
 def test_matvec_refusals(lib, kw, w, code):
     a = dict(x=16, T=2, K=64, N=8, out=16, dtype=FP32)
