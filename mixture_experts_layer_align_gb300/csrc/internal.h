@@ -174,8 +174,10 @@ struct W4View {
   int scale_bf16;
   int group;             // 32, 64 or 128
 };
-cudaError_t launch_w4_matvec(const __nv_bfloat16* x, int T, int K, int N, const W4View& w,
-                             void* out, bool out_fp32, cudaStream_t st);
+// map: the codes as bytes [rows][K/2], boxes of 128 bytes x 64 rows, 128-byte swizzle.
+cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int T, int K, int N,
+                             const W4View& w, void* out, bool out_fp32,
+                             unsigned long long timeout_ns, int num_sms, cudaStream_t st);
 struct W4LayerParams {
   const __nv_bfloat16* x;
   W4View w13, w2;
@@ -187,10 +189,13 @@ struct W4LayerParams {
   __nv_bfloat16* h;             // [T*k][I]
   float* y;                     // [T*k][H]
   __nv_bfloat16* out;
+  int* err;                     // status word
+  unsigned long long timeout_ns;
 };
 // Rows of an alignment block: the pairs of one expert that one thread block takes.
 int w4_block_rows(int T);
-cudaError_t launch_w4_layer(const W4LayerParams& p, cudaStream_t st);
+cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
+                            const W4LayerParams& p, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------ grouped GEMM
 struct GemmParams {

@@ -729,7 +729,8 @@ bool w4_sizes_ok(int T, int H, int I, int E, int k) {
 
 bool w4_sizes_supported(int T, int H, int I, int k) {
   const long long P = static_cast<long long>(T) * k;
-  return H % 32 == 0 && I % 32 == 0 && P < (1ll << 31) / 2 && H < (1 << 19) && I < (1 << 18);
+  return H % 32 == 0 && I % 32 == 0 && P < (1ll << 31) / 2 && H < (1 << 19) && I < (1 << 18) &&
+         P * H < (1ll << 36) && P * I < (1ll << 36);
 }
 
 struct W4Layout {
@@ -834,8 +835,11 @@ moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tens
   DeviceInfo dev;
   st = check_device(&dev);
   if (st != MOE_OK) return st;
-  return launch_w4_matvec(static_cast<const __nv_bfloat16*>(x), T, K, N, w4_view(*w), out,
-                          out_dtype == MOE_DT_FP32, stream) == cudaSuccess
+  CUtensorMap map;
+  if (!make_tmap(&map, w->codes, false, K / 2, N, 64)) return MOE_ERR_CUDA;
+  return launch_w4_matvec(map, static_cast<const __nv_bfloat16*>(x), T, K, N, w4_view(*w), out,
+                          out_dtype == MOE_DT_FP32, kWaitLimitNs, dev.num_sms,
+                          stream) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -903,7 +907,14 @@ moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t worksp
   p.h = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
   p.y = reinterpret_cast<float*>(ws + L.y);
   p.out = static_cast<__nv_bfloat16*>(a->out);
-  return launch_w4_layer(p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  p.err = &reinterpret_cast<Ctrl*>(ws + L.ctrl)->err;
+  p.timeout_ns = kWaitLimitNs;
+  CUtensorMap map13, map2;
+  if (!make_tmap(&map13, a->w13.codes, false, H / 2, static_cast<uint64_t>(E) * 2 * I, 64) ||
+      !make_tmap(&map2, a->w2.codes, false, I / 2, static_cast<uint64_t>(E) * H, 64))
+    return MOE_ERR_CUDA;
+  return launch_w4_layer(map13, map2, p, dev.num_sms, stream) == cudaSuccess ? MOE_OK
+                                                                             : MOE_ERR_CUDA;
 }
 
 moe_status_t moe_check_status(const void* workspace, moe_stream_t stream) {

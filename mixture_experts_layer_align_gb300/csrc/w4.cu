@@ -2,11 +2,16 @@
 // products of the MoE layer for a few tokens.
 //
 // y[t][r] = sum over groups of scale[r][group] * sum_k x[t][k] (code[r][k] - zero[r][group]).
-// What bounds it at a few tokens is reading the codes once.  They go from
-// global memory to a per-warp ring in shared memory (cp.async), become bf16
-// (code - zero is a small integer: exact) in registers and are the A operand
-// (16 weight rows) of mma.m16n8k16 with 8 tokens in N, so that the products
-// cost the same for one token as for eight; a group's sum is scaled in fp32.
+// At a few tokens the codes' bytes bound it, if turning them into an MMA operand
+// does not: at 6.8 TB/s an SM takes in 47 codes a clock.
+//
+// A thread block owns 128 weight rows and a slice of K; the blocks of a cluster
+// share rows and split K.  TMA brings 256 columns of the rows (128 bytes each) a
+// stage; four warps, a thread per row, turn 32 codes at a time into bf16 (code -
+// zero is a small integer: exact) and put them into tensor memory, where they
+// are the A operand (128 rows) of tcgen05.mma with the tokens in N; x goes to
+// shared memory.  The accumulators of each group come back, again a thread per
+// row, and are scaled in fp32: no weight is rounded.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -19,40 +24,12 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;   // K blocks of a warp in its ring
-constexpr int kBlockK = 128; // columns of one K block: 16 bytes of a row for each of 4 lanes
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Four 8 x 16-byte matrices: lane (g, i) gets 4-byte word i of row g of each;
-// lane 8 j + r gives the shared-memory address of row r of matrix j.
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
-
-// D = A B + C, 16 x 8 x 16, bf16 in, fp32 accumulators.
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1, const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
-        "f"(c[2]), "f"(c[3]));
-}
+constexpr int kRows = 128;       // weight rows of a thread block (64 gate and 64 up rows)
+constexpr int kStepK = 256;      // columns of a stage
+constexpr int kStages = 3;
+constexpr int kStageBytes = kRows * kStepK / 2;
+constexpr int kWorkers = 128;    // threads that convert: one per row
+constexpr int kThreads = kWorkers + 32;
 
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
@@ -65,7 +42,7 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 // exponents share their spacing), so a masked nibble needs one fused
 // multiply-add: x 2^127 (bits 0..3) or 2^123 (bits 4..7), - zero 2^-6, all exact.
 // nz holds -zero 2^-6 in both halves; the 2^6 is made good when sums are stored.
-__device__ __forceinline__ void w4_pairs(uint32_t w, uint32_t nz, uint32_t (&v)[4]) {
+__device__ __forceinline__ void w4_pairs(uint32_t w, uint32_t nz, uint32_t* v) {
   const uint32_t h = w >> 8;
   v[0] = fma_bf16x2(w & 0x000f000fu, 0x7f007f00u, nz);
   v[1] = fma_bf16x2(w & 0x00f000f0u, 0x7d007d00u, nz);
@@ -79,335 +56,338 @@ __device__ __forceinline__ uint32_t w4_neg_zero(uint32_t z) {
   return fma_bf16x2(z * 0x00010001u, 0xff00ff00u, 0x80008000u);
 }
 
-// The weight rows of a warp's MR m-tiles: where row 0 of each lies (a row of a
-// tile is a 32-bit offset away) and how many rows from there exist.
-template <int MR>
-struct W4Rows {
-  const uint8_t* codes[MR];
-  const uint8_t* scales[MR];  // bf16 or fp32
-  const uint8_t* zeros[MR];
-  int last[MR];  // index of the last row that exists, >= 0
+enum W4Mode { kMatvec, kGateUp, kDown };
+struct W4Job {
+  const void* scales;
+  const uint8_t* zeros;
+  int scale_bf16;
+  int mode, K;
+  int n_rows;    // rows of the result: N, I or H
+  int n_blocks;  // blocks of tokens (an upper bound for the layer)
+  const __nv_bfloat16* x;  // tokens, or h by pair (down)
+  int T;
+  void* out;     // matvec: [T][N]; gate/up: h bf16 [pair][I]; down: y fp32 [pair][H]
+  int out_fp32;
+  int cluster;   // thread blocks that split K
+  // layer
+  const int32_t* sorted_ids;
+  const int32_t* block_expert;
+  const int32_t* num_padded;
+  const float* wts;
+  int P, k;
+  int* err;      // status word, or null
+  unsigned long long timeout_ns;
 };
 
-template <int MR>
-__device__ __forceinline__ void w4_rows(W4Rows<MR>& t, int m, const W4View& w, int K, int groups,
-                                        size_t row, int last) {
-  t.codes[m] = w.codes + row * (K / 2);
-  t.scales[m] = static_cast<const uint8_t*>(w.scales) + row * groups * (w.scale_bf16 ? 2 : 4);
-  t.zeros[m] = w.zeros ? w.zeros + row * groups : nullptr;
-  t.last[m] = last;
-}
-
-// One warp: acc[m][n] += rows x tokens over the K blocks wk, wk + WK, ...
-//   xp[n]: this lane's token (8 n + g, or any other where there is none: its
-//   column of the result is not used); ring: this warp's kStages * MR * 1024 bytes
-// A K block of 16 rows is 64 16-byte pieces: piece c of row g (columns 32 c ..)
-// sits at 16-byte slot 4 g + (c ^ (g >> 1 & 3)), so that both the copies and
-// ldmatrix are free of bank conflicts.  ldmatrix gives lane (g, i) word i of
-// piece c (columns 32 c + 8 i ..), so every mma sums columns of one piece, hence
-// of one group.  Inside a word the columns come in the codes' order ((0,4),
-// (1,5), ...), and x is permuted to match.
-template <int PG, int MR, int NT>  // PG: pieces of a group, 1, 2 or 4
-__device__ __forceinline__ void w4_warp_tile(const W4Rows<MR>& t, bool scale_bf16, int K,
-                                             const __nv_bfloat16* const (&xp)[NT], int wk, int WK,
-                                             uint32_t ring, float (&acc)[MR][NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const int groups = (K + 32 * PG - 1) / (32 * PG);
-  const int nb = (K + kBlockK - 1) / kBlockK;
-  const int n_iter = nb > wk ? (nb - wk + WK - 1) / WK : 0;
-  const bool zeros = t.zeros[0] != nullptr;
-  const uint32_t put = ring + (g * 4 + (tig ^ ((g >> 1) & 3))) * 16;
-  // ldmatrix: lane 8 c + r addresses piece c of row r
-  const uint32_t get = ring + (lane & 7) * 64 + ((lane >> 3) ^ ((lane >> 1) & 3)) * 16;
-
-  uint32_t code_at[MR][2], group_at[MR][2];
-#pragma unroll
-  for (int m = 0; m < MR; ++m)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint32_t row = min(g + 8 * r, t.last[m]);
-      code_at[m][r] = row * (K / 2) + wk * 64 + tig * 16;
-      group_at[m][r] = row * groups + (wk * 4 + tig) / PG;
-    }
-  auto issue = [&](int i) {
-    if (i < n_iter && (wk + i * WK) * kBlockK + tig * 32 < K) {
-      const uint32_t dst = put + (i % kStages) * (MR * 1024);
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          cp_async16(dst + m * 1024 + r * 512, t.codes[m] + (code_at[m][r] + i * WK * 64));
-    }
-    cp_async_commit();
-  };
-  uint32_t s_nx[MR][2] = {}, z_nx[MR][2] = {};
-  // lane tig holds the scale of piece tig's group (all four lanes when the block
-  // is one group)
-  auto fetch_scales = [&](int i) {
-    if (i < n_iter && (PG == 4 || (wk + i * WK) * kBlockK + tig * 32 < K)) {
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t at = group_at[m][r] + i * WK * (4 / PG);
-          s_nx[m][r] = scale_bf16
-                           ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(t.scales[m]) + at)) << 16
-                           : __ldg(reinterpret_cast<const uint32_t*>(t.scales[m]) + at);
-          if (zeros) z_nx[m][r] = __ldg(t.zeros[m] + at);
-        }
-    }
-  };
-  uint4 x_nx[NT];
-  auto fetch_x = [&](int col) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      x_nx[n] = __ldg(reinterpret_cast<const uint4*>(xp[n] + col + tig * 8));
-  };
-
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
-  if (n_iter > 0) {
-    fetch_scales(0);
-    fetch_x(wk * kBlockK);
-  }
-  float part[MR][NT][4];
-  const float none[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int i = 0; i < n_iter; ++i) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();  // every lane's copies of stage i have landed, and stage i - 1 is read
-    issue(i + kStages - 1);
-    const int col0 = (wk + i * WK) * kBlockK;
-    const int pieces = min(4, (K - col0) / 32);
-    uint32_t q[MR][2][4];
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        ldmatrix4(q[m][r], get + (i % kStages) * (MR * 1024) + m * 1024 + r * 512);
-    float s[MR][2];
-    uint32_t z[MR][2];
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        s[m][r] = __uint_as_float(s_nx[m][r]);
-        z[m][r] = zeros ? w4_neg_zero(z_nx[m][r]) : kNegEight;
-      }
-    fetch_scales(i + 1);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c < pieces) {
-        uint32_t b[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          b[n][0] = __byte_perm(x_nx[n].x, x_nx[n].z, 0x5410);
-          b[n][1] = __byte_perm(x_nx[n].x, x_nx[n].z, 0x7632);
-          b[n][2] = __byte_perm(x_nx[n].y, x_nx[n].w, 0x5410);
-          b[n][3] = __byte_perm(x_nx[n].y, x_nx[n].w, 0x7632);
-        }
-        if (c + 1 < pieces) fetch_x(col0 + (c + 1) * 32);
-        else if (i + 1 < n_iter) fetch_x(col0 + WK * kBlockK);
-        const int from = (lane & ~3) | c;  // the lane that holds this piece's scale
-#pragma unroll
-        for (int m = 0; m < MR; ++m) {
-          uint32_t z0 = z[m][0], z1 = z[m][1];
-          if (PG < 4 && zeros) {
-            z0 = __shfl_sync(0xffffffffu, z0, from);
-            z1 = __shfl_sync(0xffffffffu, z1, from);
-          }
-          uint32_t v0[4], v1[4];
-          w4_pairs(q[m][0][c], z0, v0);
-          w4_pairs(q[m][1][c], z1, v1);
-          const uint32_t a0[4] = {v0[0], v1[0], v0[1], v1[1]}, a1[4] = {v0[2], v1[2], v0[3], v1[3]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (c % PG == 0) mma_bf16(part[m][n], a0, b[n][0], b[n][1], none);
-            else mma_bf16(part[m][n], a0, b[n][0], b[n][1], part[m][n]);
-            mma_bf16(part[m][n], a1, b[n][2], b[n][3], part[m][n]);
-          }
-          if (c % PG == PG - 1 || c + 1 == pieces) {
-            const float s0 = PG < 4 ? __shfl_sync(0xffffffffu, s[m][0], from) : s[m][0];
-            const float s1 = PG < 4 ? __shfl_sync(0xffffffffu, s[m][1], from) : s[m][1];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              acc[m][n][0] = fmaf(s0, part[m][n][0], acc[m][n][0]);
-              acc[m][n][1] = fmaf(s0, part[m][n][1], acc[m][n][1]);
-              acc[m][n][2] = fmaf(s1, part[m][n][2], acc[m][n][2]);
-              acc[m][n][3] = fmaf(s1, part[m][n][3], acc[m][n][3]);
-            }
-          }
-        }
-      }
-    }
-  }
-  cp_async_wait<0>();
-}
-
-// Sums the warps' accumulators over the WK warps that share rows, in shared
-// memory: red[wk][(wr * MR + m) * 16 + row][8 NT] (the rings' space).
-template <int MR, int NT>
-__device__ __forceinline__ void w4_store_partials(float* red, int wk, int wr, int WR,
-                                                  const float (&acc)[MR][NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-#pragma unroll
-  for (int m = 0; m < MR; ++m) {
-    float* p = red + (static_cast<size_t>(wk) * WR * MR + wr * MR + m) * 16 * 8 * NT;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      p[g * 8 * NT + n * 8 + tig * 2] = 64.f * acc[m][n][0];
-      p[g * 8 * NT + n * 8 + tig * 2 + 1] = 64.f * acc[m][n][1];
-      p[(g + 8) * 8 * NT + n * 8 + tig * 2] = 64.f * acc[m][n][2];
-      p[(g + 8) * 8 * NT + n * 8 + tig * 2 + 1] = 64.f * acc[m][n][3];
-    }
-  }
-}
-template <int MR, int NT>
-__device__ __forceinline__ float w4_sum_partials(const float* red, int WK, int WR, int row,
-                                                 int tok) {
-  float v = 0.f;
-  for (int i = 0; i < WK; ++i)
-    v += red[(static_cast<size_t>(i) * WR * MR * 16 + row) * 8 * NT + tok];
-  return v;
-}
-
-template <int MR>
-constexpr size_t w4_smem() {
-  return static_cast<size_t>(kWarps) * kStages * MR * 1024;
-}
-static_assert(w4_smem<1>() >= size_t(kWarps) * 16 * 32 * 4, "partials fit the rings");
-
-// ---------------------------------------------------------------- matvec
-template <int PG, int MR, int NT>
-__global__ void __launch_bounds__(kThreads)
-    w4_matvec_kernel(const __nv_bfloat16* __restrict__ x, int T, int K, int N, W4View w,
-                     void* __restrict__ out, int out_fp32, int WK) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-  const int WR = kWarps / WK, wk = warp % WK, wr = warp / WK;
-  pdl_wait();
-  pdl_trigger();
-  const int rows = WR * MR * 16;
-  const long long r0 = static_cast<long long>(blockIdx.x) * rows;
-  const int t0 = blockIdx.y * 8 * NT;
-  const int groups = (K + 32 * PG - 1) / (32 * PG);
-  W4Rows<MR> t;
-#pragma unroll
-  for (int m = 0; m < MR; ++m) {
-    const long long row = min(r0 + (wr * MR + m) * 16, static_cast<long long>(N) - 1);
-    w4_rows(t, m, w, K, groups, row, static_cast<int>(min(N - 1 - row, 15ll)));
-  }
-  const __nv_bfloat16* xp[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) xp[n] = x + static_cast<size_t>(min(t0 + n * 8 + g, T - 1)) * K;
-  float acc[MR][NT][4] = {};
-  w4_warp_tile<PG, MR, NT>(t, w.scale_bf16, K, xp, wk, WK,
-                           smem_addr(smem) + warp * (kStages * MR * 1024), acc);
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);
-  w4_store_partials<MR, NT>(red, wk, wr, WR, acc);
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * 8 * NT; i += kThreads) {
-    const int tok = i / rows, r = i - tok * rows;
-    if (t0 + tok < T && r0 + r < N) {
-      const float v = w4_sum_partials<MR, NT>(red, WK, WR, r, tok);
-      const size_t o = static_cast<size_t>(t0 + tok) * N + r0 + r;
-      if (out_fp32) static_cast<float*>(out)[o] = v;
-      else static_cast<__nv_bfloat16*>(out)[o] = __float2bfloat16_rn(v);
-    }
-  }
-}
-
-// ---------------------------------------------------------------- layer
-// Gate/up products of one alignment block (up to 8 NT pairs of one expert) and
-// 16 WR rows of I: h[p][i] = SiLU(gate) * up, bf16 (the down product's operand).
 template <int PG, int NT>
-__global__ void __launch_bounds__(kThreads) w4_gate_up_kernel(W4LayerParams p, int WK) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-  const int WR = kWarps / WK, wk = warp % WK, wr = warp / WK;
+struct W4Shape {
+  static constexpr int kN = NT < 16 ? 16 : NT;  // MMA N (16 at least with 128 rows)
+  // columns of a unit: what is converted, multiplied and accumulated at a time
+  static constexpr int kUnitK = NT == 64 && PG == 1 ? 64 : 128;
+  static constexpr int kSub = kUnitK / (32 * PG);  // groups, so accumulators, of a unit
+  static constexpr int kACols = kUnitK / 2;
+  static constexpr int kUsed = kACols + kN * kSub;
+  static constexpr int kTmem = kUsed <= 128 ? 128 : 256;
+  static_assert(kUsed <= 256, "tensor memory of a thread block");
+  static constexpr int kXBytes = kN * kUnitK * 2;
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kXBytes + 1024;
+  static constexpr int kPerSm = NT <= 16 ? 4 : NT == 32 ? 3 : 2;
+};
+
+// PG: 32-column pieces of a group (1, 2, 4).  NT: tokens of a block at most.
+template <int PG, bool ZP, int NT>
+__global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
+    w4_kernel(const __grid_constant__ CUtensorMap map, const W4Job j) {
+  using S = W4Shape<PG, NT>;
+  constexpr int kUnits = kStepK / S::kUnitK;  // units of a stage
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t s_full[kStages], s_a_full, s_d_full;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  uint8_t* s_x = smem + kStages * kStageBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int CS = j.cluster;
+  const int rank = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  if (tid == 0) {
+    prefetch_tensormap(&map);
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[i], 1);
+    mbar_init(&s_a_full, kWorkers / 32);
+    mbar_init(&s_d_full, 1);
+    s_abort = 0;
+    fence_mbarrier_init();
+  }
   pdl_wait();
   pdl_trigger();
-  const int block = blockIdx.x;
-  if (block * 8 * NT >= __ldg(p.num_padded)) return;
-  const int e = __ldg(p.block_expert + block);
-  const int32_t* pairs = p.sorted_ids + static_cast<size_t>(block) * 8 * NT;
-  const int P = p.T * p.k;
-  const int i0 = blockIdx.y * WR * 16;
-  const int groups = (p.H + 32 * PG - 1) / (32 * PG);
-  W4Rows<2> t;
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const int i = min(i0 + wr * 16, p.I - 1);
-    w4_rows(t, m, p.w13, p.H, groups,
-            static_cast<size_t>(e) * 2 * p.I + static_cast<size_t>(m) * p.I + i,
-            min(p.I - 1 - i, 15));
+
+  // which rows and tokens; a block past the layer's last one leaves (all of its
+  // cluster does)
+  const int job = static_cast<int>(blockIdx.x) / CS;
+  const int block = job % j.n_blocks;
+  const int r0 = job / j.n_blocks * (j.mode == kGateUp ? kRows / 2 : kRows);
+  int e = 0, valid;
+  if (j.mode == kMatvec) {
+    valid = min(NT, j.T - block * NT);
+  } else {
+    if (block * NT >= __ldg(j.num_padded)) return;
+    e = __ldg(j.block_expert + block);
+    const int32_t* ids = j.sorted_ids + static_cast<size_t>(block) * NT;
+    valid = __popc(__ballot_sync(0xffffffffu, lane < NT && __ldg(ids + min(lane, NT - 1)) < j.P));
+    if (NT > 32) valid += __popc(__ballot_sync(0xffffffffu, __ldg(ids + NT - 32 + lane) < j.P));
   }
-  const __nv_bfloat16* xp[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int pair = min(__ldg(pairs + n * 8 + g), P - 1);
-    xp[n] = p.x + static_cast<size_t>(pair / p.k) * p.H;
+  if (warp == 4) {
+    tmem_alloc(&s_tmem, S::kTmem);
+    tmem_relinquish();
   }
-  float acc[2][NT][4] = {};
-  w4_warp_tile<PG, 2, NT>(t, p.w13.scale_bf16, p.H, xp, wk, WK,
-                          smem_addr(smem) + warp * (kStages * 2 * 1024), acc);
   __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);
-  w4_store_partials<2, NT>(red, wk, wr, WR, acc);
-  __syncthreads();
-  for (int i = threadIdx.x; i < WR * 16 * 8 * NT; i += kThreads) {
-    const int tok = i / (WR * 16), r = i - tok * (WR * 16);
-    const int pair = __ldg(pairs + tok);
-    if (pair < P && i0 + r < p.I) {
-      const int rr = (r / 16) * 32 + r % 16;  // the row's gate m-tile
-      const float gate = w4_sum_partials<2, NT>(red, WK, WR, rr, tok);
-      const float up = w4_sum_partials<2, NT>(red, WK, WR, rr + 16, tok);
-      p.h[static_cast<size_t>(pair) * p.I + i0 + r] =
-          __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
+  tc_fence_after_sync();
+  const uint32_t tmem = s_tmem, t_a = tmem, t_d = tmem + S::kACols;
+  const size_t row_a = (j.mode == kGateUp ? static_cast<size_t>(e) * 2 : static_cast<size_t>(e)) *
+                           j.n_rows + r0;
+  const size_t row_b = row_a + (j.mode == kGateUp ? j.n_rows : kRows / 2);
+
+  // this block's slice of K, in stages and units
+  const int all_steps = (j.K + kStepK - 1) / kStepK;
+  const int step0 = static_cast<int>(static_cast<long long>(rank) * all_steps / CS);
+  const int step1 = static_cast<int>(static_cast<long long>(rank + 1) * all_steps / CS);
+  const int n_steps = step1 - step0;
+  const int k0 = step0 * kStepK, k1 = min(step1 * kStepK, j.K);
+  const int n_units = (k1 - k0 + S::kUnitK - 1) / S::kUnitK;
+
+  float acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      auto issue = [&](int step) {
+        uint64_t* bar = &s_full[step % kStages];
+        uint8_t* dst = smem + step % kStages * kStageBytes;
+        mbar_arrive_expect_tx(bar, kStageBytes);
+        const int col = (step0 + step) * (kStepK / 2);
+        tma_load_2d(dst, &map, bar, col, static_cast<int>(row_a));
+        tma_load_2d(dst + kStageBytes / 2, &map, bar, col, static_cast<int>(row_b));
+      };
+      int issued = min(kStages, n_steps);
+      for (int i = 0; i < issued; ++i) issue(i);
+      const uint32_t idesc = umma_idesc(true, kRows, S::kN);
+      const uint64_t db = sdesc_kmajor_sw128(smem_addr(s_x));
+      bool ok = true;
+      for (int u = 0; u < n_units; ++u) {
+        ok = mbar_wait(&s_a_full, u & 1, &s_abort, j.timeout_ns);
+        if (!ok) break;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < S::kUnitK / 16; ++i) {
+          // 16 columns: 32 bytes further in a token's 128-byte row, or its next row block
+          const uint64_t b = db + (i % 4) * 2 + (i / 4) * (S::kN * 128 / 16);
+          umma_bf16_ts(t_d + i / (2 * PG) * S::kN, t_a + i * 8, b, idesc, i % (2 * PG) != 0);
+        }
+        umma_commit(&s_d_full);
+        // every warp has read the unit's codes: its stage is free after the last one
+        if ((u + 1) % kUnits == 0 && issued < n_steps) issue(issued++);
+      }
+      if (!ok) {
+        s_abort = 1;
+        if (j.err != nullptr) atomicOr(j.err, kDevErrTimeout);
+        // the copies in flight land before the block leaves
+        volatile int never = 0;
+        for (int i = max(0, issued - kStages); i < issued; ++i)
+          mbar_wait(&s_full[i % kStages], i / kStages & 1, &never, j.timeout_ns);
+      }
+    }
+  } else {
+    const int row = tid;  // of the block's 128
+    const size_t grow =
+        min((row < kRows / 2 ? row_a : row_b - kRows / 2) + row,
+            // a row past the result's last one takes that one's scales
+            static_cast<size_t>(j.mode == kGateUp ? 2 * e + (row >= kRows / 2) : e) * j.n_rows +
+                j.n_rows - 1);
+    const int groups = (j.K + 32 * PG - 1) / (32 * PG);
+    const size_t group0 = grow * groups + k0 / (32 * PG);
+    // tokens: 16-byte piece tid % (kUnitK / 8) of token tid / (kUnitK / 8), ...
+    constexpr int kPieces = S::kUnitK / 8, kPerRound = kWorkers / kPieces;
+    constexpr int kRounds = (NT + kPerRound - 1) / kPerRound;
+    const int piece = tid % kPieces;
+    const __nv_bfloat16* xp[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int t = min(tid / kPieces + i * kPerRound, valid - 1);
+      size_t at;
+      if (j.mode == kMatvec) {
+        at = static_cast<size_t>(block) * NT + t;
+      } else {
+        const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
+        at = j.mode == kGateUp ? pair / j.k : pair;
+      }
+      xp[i] = j.x + at * j.K + k0 + piece * 8;
+    }
+    uint4 x_nx[kRounds];
+    auto fetch_x = [&](int u) {
+      const bool on = u < n_units && k0 + u * S::kUnitK + piece * 8 < k1;
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i)
+        x_nx[i] = on ? __ldg(reinterpret_cast<const uint4*>(xp[i] + u * S::kUnitK))
+                     : make_uint4(0, 0, 0, 0);
+    };
+    float s_nx[S::kSub];
+    uint32_t z_nx[S::kSub];
+    auto fetch_scales = [&](int u) {
+#pragma unroll
+      for (int i = 0; i < S::kSub; ++i) {
+        const int g = u * S::kSub + i;
+        if (u < n_units && k0 + g * (32 * PG) < k1) {
+          s_nx[i] = j.scale_bf16
+                        ? __uint_as_float(static_cast<uint32_t>(__ldg(
+                              static_cast<const uint16_t*>(j.scales) + group0 + g)) << 16)
+                        : __ldg(static_cast<const float*>(j.scales) + group0 + g);
+          if (ZP) z_nx[i] = __ldg(j.zeros + group0 + g);
+        } else {
+          s_nx[i] = 0.f;
+          if (ZP) z_nx[i] = 0;
+        }
+      }
+    };
+    fetch_scales(0);
+    fetch_x(0);
+    float s_cur[S::kSub];
+    // adds the finished accumulators of unit u, scaled
+    auto flush = [&](int u) {
+      if (!mbar_wait(&s_d_full, u & 1, &s_abort, j.timeout_ns)) return false;
+      tc_fence_after_sync();
+      const uint32_t at = t_d + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll
+      for (int i = 0; i < S::kSub; ++i)
+#pragma unroll
+        for (int t0 = 0; t0 < NT; t0 += 16) {
+          uint32_t d[2][8];
+          tmem_ld8_async(at + i * S::kN + t0, d[0]);
+          if (NT > 8) tmem_ld8_async(at + i * S::kN + t0 + 8, d[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int t = 0; t < (NT > 8 ? 16 : 8); ++t)
+            acc[t0 + t] = fmaf(s_cur[i], __uint_as_float(d[t / 8][t % 8]), acc[t0 + t]);
+        }
+      return true;
+    };
+    const uint32_t a_at = t_a + (static_cast<uint32_t>(warp * 32) << 16);
+    bool ok = true;
+    for (int u = 0; u < n_units; ++u) {
+      const int step = u / kUnits;
+      if (u % kUnits == 0) {
+        ok = mbar_wait(&s_full[step % kStages], step / kStages & 1, &s_abort, j.timeout_ns);
+        if (!ok) break;
+      }
+      const uint8_t* codes = smem + step % kStages * kStageBytes + row * 128;
+      float s[S::kSub];
+      uint32_t nz[S::kSub];
+#pragma unroll
+      for (int i = 0; i < S::kSub; ++i) {
+        s[i] = s_nx[i];
+        nz[i] = ZP ? w4_neg_zero(z_nx[i]) : kNegEight;
+      }
+      fetch_scales(u + 1);
+      // 32 columns of the row: 16 words of A
+      auto convert = [&](int c, uint32_t (&v)[16]) {
+        const uint4 q = *reinterpret_cast<const uint4*>(
+            codes + ((u % kUnits * (S::kUnitK / 32) + c) ^ (row & 7)) * 16);
+        w4_pairs(q.x, nz[c / PG], v);
+        w4_pairs(q.y, nz[c / PG], v + 4);
+        w4_pairs(q.z, nz[c / PG], v + 8);
+        w4_pairs(q.w, nz[c / PG], v + 12);
+      };
+      uint32_t v0[16], v1[16];
+      convert(0, v0);
+      convert(1, v1);
+      if (u > 0) {
+        ok = flush(u - 1);  // and the MMAs that read A and x are done
+        if (!ok) break;
+      }
+      tmem_st16(a_at, v0);
+      tmem_st16(a_at + 16, v1);
+      if (S::kUnitK == 128) {
+        convert(2, v0);
+        convert(3, v1);
+        tmem_st16(a_at + 32, v0);
+        tmem_st16(a_at + 48, v1);
+      }
+      // x, its columns in the order of the codes: (0,4), (1,5), (2,6), (3,7)
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int t = tid / kPieces + i * kPerRound;
+        const uint4 x = x_nx[i];
+        uint4 v;
+        v.x = __byte_perm(x.x, x.z, 0x5410);
+        v.y = __byte_perm(x.x, x.z, 0x7632);
+        v.z = __byte_perm(x.y, x.w, 0x5410);
+        v.w = __byte_perm(x.y, x.w, 0x7632);
+        *reinterpret_cast<uint4*>(s_x + piece / 8 * (S::kN * 128) + t * 128 +
+                                  ((piece % 8) ^ (t & 7)) * 16) = v;
+      }
+      fetch_x(u + 1);
+      fence_proxy_async_smem();
+      tmem_wait_st();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_a_full);
+#pragma unroll
+      for (int i = 0; i < S::kSub; ++i) s_cur[i] = s[i];
+    }
+    if (ok && n_units > 0) ok = flush(n_units - 1);
+    if (!ok) {
+      s_abort = 1;
+      if (j.err != nullptr && lane == 0) atomicOr(j.err, kDevErrTimeout);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t] = __int_as_float(0x7fc00000);  // a wrong sum shows
     }
   }
-}
-
-// Down products: y[p][r] = weight of pair p * (w2[e] h[p])[r], fp32.
-template <int PG, int MR, int NT>
-__global__ void __launch_bounds__(kThreads) w4_down_kernel(W4LayerParams p, int WK) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-  const int WR = kWarps / WK, wk = warp % WK, wr = warp / WK;
-  pdl_wait();
-  pdl_trigger();
-  const int block = blockIdx.x;
-  if (block * 8 * NT >= __ldg(p.num_padded)) return;
-  const int e = __ldg(p.block_expert + block);
-  const int32_t* pairs = p.sorted_ids + static_cast<size_t>(block) * 8 * NT;
-  const int P = p.T * p.k;
-  const int rows = WR * MR * 16, r0 = blockIdx.y * rows;
-  const int groups = (p.I + 32 * PG - 1) / (32 * PG);
-  W4Rows<MR> t;
-#pragma unroll
-  for (int m = 0; m < MR; ++m) {
-    const int r = min(r0 + (wr * MR + m) * 16, p.H - 1);
-    w4_rows(t, m, p.w2, p.I, groups, static_cast<size_t>(e) * p.H + r, min(p.H - 1 - r, 15));
-  }
-  const __nv_bfloat16* xp[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-    xp[n] = p.h + static_cast<size_t>(min(__ldg(pairs + n * 8 + g), P - 1)) * p.I;
-  float acc[MR][NT][4] = {};
-  w4_warp_tile<PG, MR, NT>(t, p.w2.scale_bf16, p.I, xp, wk, WK,
-                           smem_addr(smem) + warp * (kStages * MR * 1024), acc);
+  __syncwarp();
+  tc_fence_before_sync();
   __syncthreads();
+  if (warp == 4) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, S::kTmem);
+  }
+  // the sums over the cluster's slices of K, in rank order, in the stages' space:
+  // red[token][row]
   float* red = reinterpret_cast<float*>(smem);
-  w4_store_partials<MR, NT>(red, wk, wr, WR, acc);
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * 8 * NT; i += kThreads) {
-    const int tok = i / rows, r = i - tok * rows;
-    const int pair = __ldg(pairs + tok);
-    if (pair < P && r0 + r < p.H)
-      p.y[static_cast<size_t>(pair) * p.H + r0 + r] =
-          __ldg(p.wts + pair) * w4_sum_partials<MR, NT>(red, WK, WR, r, tok);
+  if (warp < 4) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) red[t * kRows + tid] = 64.f * acc[t];
   }
+  if (CS > 1) cluster_sync();
+  else __syncthreads();
+  const uint32_t red_at = smem_addr(red);
+  auto sum = [&](int t, int row) {
+    if (CS == 1) return red[t * kRows + row];
+    float v = 0.f;
+    for (int i = 0; i < CS; ++i)
+      v += ld_cluster_f32(mapa_shared(red_at + (t * kRows + row) * 4, i));
+    return v;
+  };
+  const int rows_out = j.mode == kGateUp ? kRows / 2 : kRows;
+  for (int i = rank * kThreads + tid; i < rows_out * valid; i += CS * kThreads) {
+    const int t = i / rows_out, r = i % rows_out;
+    if (r0 + r >= j.n_rows) continue;
+    if (j.mode == kMatvec) {
+      const float v = sum(t, r);
+      const size_t o = (static_cast<size_t>(block) * NT + t) * j.n_rows + r0 + r;
+      if (j.out_fp32) static_cast<float*>(j.out)[o] = v;
+      else static_cast<__nv_bfloat16*>(j.out)[o] = __float2bfloat16_rn(v);
+    } else {
+      const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
+      const size_t o = static_cast<size_t>(pair) * j.n_rows + r0 + r;
+      if (j.mode == kGateUp) {
+        const float gate = sum(t, r), up = sum(t, r + kRows / 2);
+        static_cast<__nv_bfloat16*>(j.out)[o] =
+            __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
+      } else {
+        static_cast<float*>(j.out)[o] = __ldg(j.wts + pair) * sum(t, r);
+      }
+    }
+  }
+  __syncwarp();
+  if (CS > 1) cluster_sync();  // no block leaves while another reads its sums
 }
 
 // out[t] = sum of its k weighted rows, in slot order.
@@ -431,94 +411,126 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Warps that share a row tile, splitting K: as many as leave each two K blocks.
-int warps_on_k(int K) {
-  const int nb = (K + kBlockK - 1) / kBlockK;
-  int wk = 1;
-  while (wk < kWarps && nb >= 2 * wk * 2) wk *= 2;
-  return wk;
+// Thread blocks that split K: as many as there is room for at a time, each with a
+// stage at least.
+int choose_cluster(int K, long long tiles, int per_sm, int num_sms) {
+  const int steps = (K + kStepK - 1) / kStepK;
+  int c = 1;
+  while (c < 8 && 2 * c <= steps && tiles * 2 * c <= static_cast<long long>(per_sm) * num_sms) c *= 2;
+  return c;
 }
 
-template <typename K>
-cudaError_t smem_limit(K kernel, size_t bytes) {
-  return checked(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(bytes)),
-                 "smem attribute");
-}
-
-template <int PG, int MR, int NT>
-cudaError_t matvec(const __nv_bfloat16* x, int T, int K, int N, const W4View& w, void* out,
-                   bool out_fp32, cudaStream_t st) {
-  const int WK = warps_on_k(K), rows = kWarps / WK * MR * 16;
-  cudaError_t e = smem_limit(w4_matvec_kernel<PG, MR, NT>, w4_smem<MR>());
+template <int PG, bool ZP, int NT>
+cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaStream_t st) {
+  using S = W4Shape<PG, NT>;
+  cudaError_t e = checked(cudaFuncSetAttribute(w4_kernel<PG, ZP, NT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(S::kSmem)),
+                          "smem attribute");
   if (e != cudaSuccess) return e;
-  return launch_pdl(w4_matvec_kernel<PG, MR, NT>,
-                    dim3((N + rows - 1) / rows, (T + 8 * NT - 1) / (8 * NT)), dim3(kThreads),
-                    w4_smem<MR>(), st, x, T, K, N, w, out, out_fp32 ? 1 : 0, WK);
+  W4Job j = job;
+  const int rows = j.mode == kGateUp ? kRows / 2 : kRows;
+  const long long tiles = (static_cast<long long>(j.n_rows) + rows - 1) / rows * j.n_blocks;
+  j.cluster = choose_cluster(j.K, tiles, S::kPerSm, num_sms);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * j.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(j.cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = j.cluster > 1 ? 2 : 1;
+  return checked(cudaLaunchKernelEx(&cfg, w4_kernel<PG, ZP, NT>, map, j), "kernel launch");
 }
 
-template <int PG>
-cudaError_t matvec_any(const __nv_bfloat16* x, int T, int K, int N, const W4View& w, void* out,
-                       bool out_fp32, cudaStream_t st) {
-  if (T <= 8) return matvec<PG, 2, 1>(x, T, K, N, w, out, out_fp32, st);
-  if (T <= 16) return matvec<PG, 2, 2>(x, T, K, N, w, out, out_fp32, st);
-  return matvec<PG, 2, 4>(x, T, K, N, w, out, out_fp32, st);
+template <int PG, bool ZP>
+cudaError_t launch_tokens(const CUtensorMap& map, const W4Job& j, int nt, int num_sms,
+                          cudaStream_t st) {
+  if (nt == 8) return launch<PG, ZP, 8>(map, j, num_sms, st);
+  if (nt == 16) return launch<PG, ZP, 16>(map, j, num_sms, st);
+  if (nt == 32) return launch<PG, ZP, 32>(map, j, num_sms, st);
+  return launch<PG, ZP, 64>(map, j, num_sms, st);
 }
 
-template <int PG, int NT>
-cudaError_t gate_up(const W4LayerParams& p, int blocks, cudaStream_t st) {
-  const int WK = warps_on_k(p.H), rows = kWarps / WK * 16;
-  cudaError_t e = smem_limit(w4_gate_up_kernel<PG, NT>, w4_smem<2>());
-  if (e != cudaSuccess) return e;
-  return launch_pdl(w4_gate_up_kernel<PG, NT>, dim3(blocks, (p.I + rows - 1) / rows),
-                    dim3(kThreads), w4_smem<2>(), st, p, WK);
+cudaError_t launch_job(const CUtensorMap& map, int group, const W4Job& j, int nt, int num_sms,
+                       cudaStream_t st) {
+  if (j.zeros != nullptr)
+    return group == 32   ? launch_tokens<1, true>(map, j, nt, num_sms, st)
+           : group == 64 ? launch_tokens<2, true>(map, j, nt, num_sms, st)
+                         : launch_tokens<4, true>(map, j, nt, num_sms, st);
+  return group == 32   ? launch_tokens<1, false>(map, j, nt, num_sms, st)
+         : group == 64 ? launch_tokens<2, false>(map, j, nt, num_sms, st)
+                       : launch_tokens<4, false>(map, j, nt, num_sms, st);
 }
 
-template <int PG, int NT>
-cudaError_t down(const W4LayerParams& p, int blocks, cudaStream_t st) {
-  const int WK = warps_on_k(p.I), rows = kWarps / WK * 2 * 16;
-  cudaError_t e = smem_limit(w4_down_kernel<PG, 2, NT>, w4_smem<2>());
-  if (e != cudaSuccess) return e;
-  return launch_pdl(w4_down_kernel<PG, 2, NT>, dim3(blocks, (p.H + rows - 1) / rows),
-                    dim3(kThreads), w4_smem<2>(), st, p, WK);
+}  // namespace
+
+int w4_block_rows(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
+cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int T, int K, int N,
+                             const W4View& w, void* out, bool out_fp32,
+                             unsigned long long timeout_ns, int num_sms, cudaStream_t st) {
+  const int nt = w4_block_rows(T);
+  W4Job j{};
+  j.scales = w.scales;
+  j.zeros = w.zeros;
+  j.scale_bf16 = w.scale_bf16;
+  j.mode = kMatvec;
+  j.K = K;
+  j.n_rows = N;
+  j.n_blocks = (T + nt - 1) / nt;
+  j.x = x;
+  j.T = T;
+  j.out = out;
+  j.out_fp32 = out_fp32 ? 1 : 0;
+  j.timeout_ns = timeout_ns;
+  return launch_job(map, w.group, j, nt, num_sms, st);
 }
 
-template <int NT>
-cudaError_t layer(const W4LayerParams& p, cudaStream_t st) {
+cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
+                            const W4LayerParams& p, int num_sms, cudaStream_t st) {
+  const int nt = w4_block_rows(p.T);
   const long long P = static_cast<long long>(p.T) * p.k;
-  const int blocks = static_cast<int>(
-      std::min(P, (P + std::min<long long>(p.E, P) * (8 * NT - 1)) / (8 * NT)));
-  cudaError_t e = p.w13.group == 32   ? gate_up<1, NT>(p, blocks, st)
-                  : p.w13.group == 64 ? gate_up<2, NT>(p, blocks, st)
-                                      : gate_up<4, NT>(p, blocks, st);
+  W4Job j{};
+  j.scales = p.w13.scales;
+  j.zeros = p.w13.zeros;
+  j.scale_bf16 = p.w13.scale_bf16;
+  j.mode = kGateUp;
+  j.K = p.H;
+  j.n_rows = p.I;
+  j.n_blocks = static_cast<int>(std::min(P, (P + std::min<long long>(p.E, P) * (nt - 1)) / nt));
+  j.x = p.x;
+  j.T = p.T;
+  j.out = p.h;
+  j.sorted_ids = p.sorted_ids;
+  j.block_expert = p.block_expert;
+  j.num_padded = p.num_padded;
+  j.wts = p.wts;
+  j.P = static_cast<int>(P);
+  j.k = p.k;
+  j.err = p.err;
+  j.timeout_ns = p.timeout_ns;
+  cudaError_t e = launch_job(map13, p.w13.group, j, nt, num_sms, st);
   if (e != cudaSuccess) return e;
-  e = p.w2.group == 32   ? down<1, NT>(p, blocks, st)
-      : p.w2.group == 64 ? down<2, NT>(p, blocks, st)
-                         : down<4, NT>(p, blocks, st);
+  j.scales = p.w2.scales;
+  j.zeros = p.w2.zeros;
+  j.scale_bf16 = p.w2.scale_bf16;
+  j.mode = kDown;
+  j.K = p.I;
+  j.n_rows = p.H;
+  j.x = p.h;
+  j.out = p.y;
+  e = launch_job(map2, p.w2.group, j, nt, num_sms, st);
   if (e != cudaSuccess) return e;
   const long long n = static_cast<long long>(p.T) * (p.H / 4);
   return launch_pdl(w4_combine_kernel,
                     dim3(static_cast<int>(std::min<long long>((n + 255) / 256, 2048))), dim3(256),
                     0, st, static_cast<const float*>(p.y), p.T, p.k, p.H, p.out);
-}
-
-}  // namespace
-
-cudaError_t launch_w4_matvec(const __nv_bfloat16* x, int T, int K, int N, const W4View& w,
-                             void* out, bool out_fp32, cudaStream_t st) {
-  if (w.group == 32) return matvec_any<1>(x, T, K, N, w, out, out_fp32, st);
-  if (w.group == 64) return matvec_any<2>(x, T, K, N, w, out, out_fp32, st);
-  return matvec_any<4>(x, T, K, N, w, out, out_fp32, st);
-}
-
-int w4_block_rows(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : 32; }
-
-cudaError_t launch_w4_layer(const W4LayerParams& p, cudaStream_t st) {
-  switch (w4_block_rows(p.T)) {
-    case 8: return layer<1>(p, st);
-    case 16: return layer<2>(p, st);
-    default: return layer<4>(p, st);
-  }
 }
 
 }  // namespace moe
