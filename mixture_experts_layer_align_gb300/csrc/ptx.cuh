@@ -25,6 +25,16 @@ __device__ __forceinline__ uint32_t lane_id() {
   return l;
 }
 
+// True in one lane of a converged warp, which the compiler knows to be one: code
+// under it keeps the operands of tcgen05 and TMA instructions in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ---------------------------------------------------------------- launch order
 // Programmatic dependent launch: wait until the preceding grid in the stream
 // has completed and its memory is visible (a no-op without the launch
