@@ -174,11 +174,8 @@ struct W4View {
   int scale_bf16;
   int group;             // 32, 64 or 128
 };
-// map: the codes as bytes [rows][K/2], boxes of 128 bytes x 64 rows; map_x: the
-// tokens bf16 [rows][K], boxes of 64 columns x w4_x_box_rows(T) rows; both with the
-// 128-byte swizzle.
-inline int w4_x_box_rows(int T) { return T == 1 ? 1 : 8; }
-cudaError_t launch_w4_matvec(const CUtensorMap& map, const CUtensorMap& map_x, int T, int K, int N,
+// map: the codes as bytes [rows][K/2], boxes of 128 bytes x 64 rows, 128-byte swizzle.
+cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int T, int K, int N,
                              const W4View& w, void* out, bool out_fp32,
                              unsigned long long timeout_ns, int num_sms, cudaStream_t st);
 struct W4LayerParams {
@@ -189,8 +186,7 @@ struct W4LayerParams {
   const int32_t* sorted_ids;    // pair ids by expert in blocks of w4_block_rows(T), T*k pads
   const int32_t* block_expert;  // expert of each block
   const int32_t* num_padded;    // rows of all blocks
-  __nv_bfloat16* xs;            // [aligned rows][H]
-  __nv_bfloat16* h;             // [aligned rows][I]
+  __nv_bfloat16* h;             // [T*k][I]
   float* y;                     // [T*k][H]
   __nv_bfloat16* out;
   int* err;                     // status word
@@ -198,8 +194,7 @@ struct W4LayerParams {
 };
 // Rows of an alignment block: the pairs of one expert that one thread block takes.
 int w4_block_rows(int T);
-cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map_x,
-                            const CUtensorMap& map2, const CUtensorMap& map_h,
+cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
                             const W4LayerParams& p, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------ grouped GEMM

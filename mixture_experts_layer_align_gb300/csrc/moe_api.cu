@@ -735,8 +735,7 @@ bool w4_sizes_supported(int T, int H, int I, int k) {
 
 struct W4Layout {
   size_t ctrl = 0, ids = 0, wts = 0, counts = 0, offsets = 0, sorted = 0, blocks = 0,
-         padded = 0, xs = 0, h = 0, y = 0, total = 0;
-  size_t rows = 0;  // of blocks that hold a pair, at most
+         padded = 0, h = 0, y = 0, total = 0;
 };
 
 W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
@@ -754,13 +753,11 @@ W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
   L.wts = take(sizeof(float) * P);
   L.counts = take(sizeof(int32_t) * E);
   L.offsets = take(sizeof(int32_t) * (E + 1));
-  L.rows = P + static_cast<size_t>(std::min<long long>(E, P)) * (bm - 1);
-  const size_t sorted = P + static_cast<size_t>(E) * (bm - 1);
-  L.sorted = take(sizeof(int32_t) * sorted);
-  L.blocks = take(sizeof(int32_t) * (sorted / bm));
+  const size_t rows = P + static_cast<size_t>(E) * (bm - 1);
+  L.sorted = take(sizeof(int32_t) * rows);
+  L.blocks = take(sizeof(int32_t) * (rows / bm));
   L.padded = take(sizeof(int32_t));
-  L.xs = take(sizeof(__nv_bfloat16) * L.rows * H);
-  L.h = take(sizeof(__nv_bfloat16) * L.rows * I);
+  L.h = take(sizeof(__nv_bfloat16) * P * I);
   L.y = take(sizeof(float) * P * H);
   L.total = off;
   return L;
@@ -838,12 +835,11 @@ moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tens
   DeviceInfo dev;
   st = check_device(&dev);
   if (st != MOE_OK) return st;
-  CUtensorMap map, map_x;
-  if (!make_tmap(&map, w->codes, false, K / 2, N, 64) ||
-      !make_tmap(&map_x, x, true, K, T, w4_x_box_rows(T)))
-    return MOE_ERR_CUDA;
-  return launch_w4_matvec(map, map_x, T, K, N, w4_view(*w), out, out_dtype == MOE_DT_FP32,
-                          kWaitLimitNs, dev.num_sms, stream) == cudaSuccess
+  CUtensorMap map;
+  if (!make_tmap(&map, w->codes, false, K / 2, N, 64)) return MOE_ERR_CUDA;
+  return launch_w4_matvec(map, static_cast<const __nv_bfloat16*>(x), T, K, N, w4_view(*w), out,
+                          out_dtype == MOE_DT_FP32, kWaitLimitNs, dev.num_sms,
+                          stream) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -855,7 +851,7 @@ size_t moe_w4_workspace_size(int T, int H, int I, int E, int top_k) {
 
 int moe_w4_launch_count(int T, int H, int I, int E, int top_k) {
   if (!w4_sizes_ok(T, H, I, E, top_k) || !w4_sizes_supported(T, H, I, top_k)) return -1;
-  return T == 0 ? 0 : 6;  // router, alignment, gather, gate/up, down, combine
+  return T == 0 ? 0 : 5;  // router, alignment, gate/up, down, combine
 }
 
 moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t workspace_bytes,
@@ -908,21 +904,17 @@ moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t worksp
   p.sorted_ids = ap.sorted_ids;
   p.block_expert = ap.tile_expert;
   p.num_padded = ap.num_padded;
-  p.xs = reinterpret_cast<__nv_bfloat16*>(ws + L.xs);
   p.h = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
   p.y = reinterpret_cast<float*>(ws + L.y);
   p.out = static_cast<__nv_bfloat16*>(a->out);
   p.err = &reinterpret_cast<Ctrl*>(ws + L.ctrl)->err;
   p.timeout_ns = kWaitLimitNs;
-  CUtensorMap map13, map_x, map2, map_h;
+  CUtensorMap map13, map2;
   if (!make_tmap(&map13, a->w13.codes, false, H / 2, static_cast<uint64_t>(E) * 2 * I, 64) ||
-      !make_tmap(&map_x, p.xs, true, H, L.rows, w4_x_box_rows(T)) ||
-      !make_tmap(&map2, a->w2.codes, false, I / 2, static_cast<uint64_t>(E) * H, 64) ||
-      !make_tmap(&map_h, p.h, true, I, L.rows, w4_x_box_rows(T)))
+      !make_tmap(&map2, a->w2.codes, false, I / 2, static_cast<uint64_t>(E) * H, 64))
     return MOE_ERR_CUDA;
-  return launch_w4_layer(map13, map_x, map2, map_h, p, dev.num_sms, stream) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  return launch_w4_layer(map13, map2, p, dev.num_sms, stream) == cudaSuccess ? MOE_OK
+                                                                             : MOE_ERR_CUDA;
 }
 
 moe_status_t moe_check_status(const void* workspace, moe_stream_t stream) {
