@@ -322,10 +322,14 @@ typedef struct {
  * Requires T >= 0 (0 enqueues nothing), N >= 1, K >= 32, K % 32 == 0
  * (MOE_ERR_UNSUPPORTED otherwise), T < 2^20, K <= 2^20, T*K and T*N < 2^31
  * (MOE_ERR_UNSUPPORTED).
- * Results do not depend on anything but the arguments (no atomics).
+ * `scratch` is a caller buffer of at least moe_w4_matvec_scratch_size(T, K) bytes,
+ * 16-byte aligned, that no other call in flight uses.  Results do not depend on
+ * anything but the arguments (no atomics).
  */
+size_t moe_w4_matvec_scratch_size(int T, int K);
 moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tensor* w, void* out,
-                           moe_dtype_t out_dtype, moe_stream_t stream);
+                           moe_dtype_t out_dtype, void* scratch, size_t scratch_bytes,
+                           moe_stream_t stream);
 
 /* Arguments of the MoE layer with 4-bit experts. */
 typedef struct {

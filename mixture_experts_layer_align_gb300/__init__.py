@@ -130,7 +130,9 @@ def load():
         L.moe_fused_forward_down.argtypes = [ctypes.POINTER(MoeFusedArgs), P, sz, P]
         L.moe_fused_h_amax_offset.argtypes = []
         L.moe_fused_h_amax_offset.restype = sz
-        L.moe_w4_matvec.argtypes = [P, i, i, i, ctypes.POINTER(MoeW4Tensor), P, i, P]
+        L.moe_w4_matvec_scratch_size.argtypes = [i, i]
+        L.moe_w4_matvec_scratch_size.restype = sz
+        L.moe_w4_matvec.argtypes = [P, i, i, i, ctypes.POINTER(MoeW4Tensor), P, i, P, sz, P]
         L.moe_w4_matvec.restype = i
         L.moe_w4_workspace_size.argtypes = [i, i, i, i, i]
         L.moe_w4_workspace_size.restype = sz
@@ -476,10 +478,15 @@ class W4Tensor:
                               MOE_DT_FP32 if scales.dtype == torch.float32 else MOE_DT_BF16, group)
 
 
-def moe_w4_matvec(x, w: W4Tensor, out=None, out_dtype=None, stream=None):
+def moe_w4_matvec_scratch_size(T: int, K: int) -> int:
+    return int(load().moe_w4_matvec_scratch_size(T, K))
+
+
+def moe_w4_matvec(x, w: W4Tensor, out=None, out_dtype=None, scratch=None, stream=None):
     """Matrix-vector products with 4-bit weights, for a few tokens: out = x w^T.
     x: bf16 [T, K]; w: W4Tensor [N, K]; out: bf16 or fp32 [T, N] (allocated, of
-    `out_dtype`, bf16 by default, when not given).  Returns out."""
+    `out_dtype`, bf16 by default, when not given); scratch: uint8,
+    moe_w4_matvec_scratch_size(T, K) bytes (allocated when not given).  Returns out."""
     import torch
     _require(x, torch.bfloat16, "x")
     if len(w.shape) != 2 or x.dim() != 2 or x.shape[1] != w.shape[1]:
@@ -492,9 +499,15 @@ def moe_w4_matvec(x, w: W4Tensor, out=None, out_dtype=None, stream=None):
     if out.dtype not in (torch.bfloat16, torch.float32) or out_dtype not in (None, out.dtype):
         raise ValueError(f"out must be bfloat16 or float32 (out_dtype {out_dtype}), got {out.dtype}")
     _require(out, out.dtype, "out", (T, N))
+    if scratch is None:
+        scratch = torch.empty(max(16, moe_w4_matvec_scratch_size(T, K)), dtype=torch.uint8,
+                              device=x.device)
+        if stream is not None:
+            scratch.record_stream(stream)
+    _require(scratch, torch.uint8, "scratch")
     _check(load().moe_w4_matvec(_ptr(x), T, K, N, ctypes.byref(w._c), _ptr(out),
                                 MOE_DT_FP32 if out.dtype == torch.float32 else MOE_DT_BF16,
-                                _stream(stream)), "moe_w4_matvec")
+                                _ptr(scratch), scratch.numel(), _stream(stream)), "moe_w4_matvec")
     return out
 
 
@@ -575,5 +588,5 @@ __all__ = ["load", "moe_fused_forward_gate_up", "moe_fused_forward_down", "h_ama
            "status_string", "MoeError", "make_step_events", "MoeFusedArgs", "MOE_DT_BF16", "MOE_DT_FP8_E4M3",
            "MOE_DEBUG_FORCE_TIMEOUT", "MOE_FLAG_TOKENS_IN_M",
            "MOE_FLAG_WEIGHTS_IN_M", "MOE_FLAG_NO_SM_PAIRS", "MOE_FLAG_ONE_KERNEL", "LIB_PATH",
-           "W4Tensor", "moe_w4_matvec", "moe_w4_forward", "moe_w4_workspace_size",
+           "W4Tensor", "moe_w4_matvec", "moe_w4_matvec_scratch_size", "moe_w4_forward", "moe_w4_workspace_size",
            "moe_w4_launch_count", "alloc_w4_workspace", "MOE_DT_FP32"]

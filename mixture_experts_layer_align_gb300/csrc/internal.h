@@ -176,8 +176,10 @@ struct W4View {
 };
 // map: the codes as bytes [rows][K/2], boxes of 128 bytes x 64 rows, 128-byte swizzle.
 cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int T, int K, int N,
-                             const W4View& w, void* out, bool out_fp32,
+                             const W4View& w, void* out, bool out_fp32, uint8_t* scratch,
                              unsigned long long timeout_ns, int num_sms, cudaStream_t st);
+// Bytes of `blocks` blocks of nt tokens with K columns, split (16-byte aligned).
+size_t w4_split_bytes(long long blocks, int nt, int K);
 struct W4LayerParams {
   const __nv_bfloat16* x;
   W4View w13, w2;
@@ -187,6 +189,7 @@ struct W4LayerParams {
   const int32_t* block_expert;  // expert of each block
   const int32_t* num_padded;    // rows of all blocks
   __nv_bfloat16* h;             // [T*k][I]
+  uint8_t *xq, *hq;             // x and h of the blocks, split
   float* y;                     // [T*k][H]
   __nv_bfloat16* out;
   int* err;                     // status word

@@ -735,7 +735,7 @@ bool w4_sizes_supported(int T, int H, int I, int k) {
 
 struct W4Layout {
   size_t ctrl = 0, ids = 0, wts = 0, counts = 0, offsets = 0, sorted = 0, blocks = 0,
-         padded = 0, h = 0, y = 0, total = 0;
+         padded = 0, h = 0, xq = 0, hq = 0, y = 0, total = 0;
 };
 
 W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
@@ -758,6 +758,11 @@ W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
   L.blocks = take(sizeof(int32_t) * (rows / bm));
   L.padded = take(sizeof(int32_t));
   L.h = take(sizeof(__nv_bfloat16) * P * I);
+  const long long pairs = static_cast<long long>(P);
+  const long long blocks =
+      std::min(pairs, (pairs + std::min<long long>(E, pairs) * (bm - 1)) / bm);
+  L.xq = take(w4_split_bytes(blocks, bm, H));
+  L.hq = take(w4_split_bytes(blocks, bm, I));
   L.y = take(sizeof(float) * P * H);
   L.total = off;
   return L;
@@ -819,8 +824,15 @@ moe_status_t moe_fused_forward_timed(const moe_fused_args* a, void* workspace,
                             reinterpret_cast<cudaEvent_t const*>(events));
 }
 
+size_t moe_w4_matvec_scratch_size(int T, int K) {
+  if (T < 1 || K < 1 || T >= (1 << 20) || K > (1 << 20)) return 0;
+  const int nt = w4_block_rows(T);
+  return w4_split_bytes((T + nt - 1) / nt, nt, K);
+}
+
 moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tensor* w, void* out,
-                           moe_dtype_t out_dtype, moe_stream_t stream) {
+                           moe_dtype_t out_dtype, void* scratch, size_t scratch_bytes,
+                           moe_stream_t stream) {
   if (T < 0 || K < 1 || N < 1 || !w) return MOE_ERR_INVALID_ARG;
   if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_FP32) return MOE_ERR_INVALID_ARG;
   moe_status_t st = check_w4(*w, T > 0);
@@ -832,14 +844,16 @@ moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tens
   if (T == 0) return MOE_OK;
   if (!x || !out || !aligned(x, 16) || !aligned(out, out_dtype == MOE_DT_FP32 ? 4 : 2))
     return MOE_ERR_INVALID_ARG;
+  if (!scratch || !aligned(scratch, 16) || scratch_bytes < moe_w4_matvec_scratch_size(T, K))
+    return MOE_ERR_WORKSPACE;
   DeviceInfo dev;
   st = check_device(&dev);
   if (st != MOE_OK) return st;
   CUtensorMap map;
   if (!make_tmap(&map, w->codes, false, K / 2, N, 64)) return MOE_ERR_CUDA;
   return launch_w4_matvec(map, static_cast<const __nv_bfloat16*>(x), T, K, N, w4_view(*w), out,
-                          out_dtype == MOE_DT_FP32, kWaitLimitNs, dev.num_sms,
-                          stream) == cudaSuccess
+                          out_dtype == MOE_DT_FP32, static_cast<uint8_t*>(scratch), kWaitLimitNs,
+                          dev.num_sms, stream) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -851,7 +865,7 @@ size_t moe_w4_workspace_size(int T, int H, int I, int E, int top_k) {
 
 int moe_w4_launch_count(int T, int H, int I, int E, int top_k) {
   if (!w4_sizes_ok(T, H, I, E, top_k) || !w4_sizes_supported(T, H, I, top_k)) return -1;
-  return T == 0 ? 0 : 5;  // router, alignment, gate/up, down, combine
+  return T == 0 ? 0 : 6;  // router, alignment, split of x, gate/up, down, combine
 }
 
 moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t workspace_bytes,
@@ -905,6 +919,8 @@ moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t worksp
   p.block_expert = ap.tile_expert;
   p.num_padded = ap.num_padded;
   p.h = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
+  p.xq = ws + L.xq;
+  p.hq = ws + L.hq;
   p.y = reinterpret_cast<float*>(ws + L.y);
   p.out = static_cast<__nv_bfloat16*>(a->out);
   p.err = &reinterpret_cast<Ctrl*>(ws + L.ctrl)->err;

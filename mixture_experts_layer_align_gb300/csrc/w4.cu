@@ -10,20 +10,20 @@
 // exponents share their spacing): the nibbles of a word, spread over bytes by two
 // masks and a shift, are the A operand of tcgen05.mma kind::f8f6f4.  x becomes three
 // E5M2 pieces whose sum it is, one MMA each into the same accumulator:
-// a power of two brings the largest |x| of 128 columns to 2^14 .. 2^15, where x is
+// a power of two brings the largest |x| of 64 columns to 2^14 .. 2^15, where x is
 // an fp16 value of 8 significant bits; a piece is the top byte of what is left (a
 // sign, 5 exponent and 2 mantissa bits: E5M2, three significant bits), so the third
 // leaves nothing but what lies 2^-31 below the largest.  Products are exact and
 // sums are fp32 (the MMA was checked to keep addends 2^-23 below the sum).
 //
-// A thread block owns 128 weight rows and a slice of K; the blocks of a cluster
-// share rows and split K.  TMA brings 256 columns of the codes (128 bytes of a row)
-// a stage.  The block's four warps, a thread per row, spread the codes of a unit
-// into tensor memory (A, 128 rows), put the pieces of x into shared memory (B) and,
-// while the unit's MMAs run, scale the sums of the unit before, again a thread per
-// row, in fp32.
+// x is split once for a call, by a kernel of its own (h by the gate/up product's
+// epilogue), into the image that shared memory needs.  A thread block owns 128
+// weight rows and a slice of K; the blocks of a cluster share rows and split K.  TMA
+// brings 256 columns of the codes (128 bytes of a row) a stage, and x block by block
+// of 128 columns.  Four warps, a thread per row, spread the codes of a unit into
+// tensor memory (A, 128 rows) and, while its MMAs run, scale the sums of the unit
+// before, again a thread per row, in fp32; a fifth warp issues the copies and MMAs.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -39,10 +39,24 @@ namespace {
 constexpr int kRows = 128;      // weight rows of a thread block (64 gate and 64 up rows)
 constexpr int kStepK = 256;     // columns of a stage
 constexpr int kStageBytes = kRows * kStepK / 2;
-constexpr int kThreads = 128;   // one per row
-constexpr int kBlockK = 128;    // columns that x is scaled and split by
+constexpr int kRowThreads = 128;  // one per row
+constexpr int kThreads = kRowThreads + 32;
+constexpr int kBlockK = 128;    // columns of a block of x
+constexpr int kScaleK = 64;     // columns of x that share a power of two
 constexpr int kPieces = 3;
+constexpr int kXSlots = 4;      // blocks of x in shared memory
 constexpr unsigned long long kDrainNs = 1000000000ull;
+
+// A block of 128 columns of nt tokens, split: kPieces x [nt][128 bytes], the 16-byte
+// chunks of token t's row at chunk ^ t % 8 (the 128-byte swizzle) and in each 8
+// columns the order of the spread codes, 0 2 4 6 1 3 5 7; then fp32 [6][nt]: 2^-9
+// times the sum of the scaled x by 32 columns (4, or the first 2 by 64), and for each
+// 64 columns the factor that undoes the scaling of x and of the codes.
+__host__ __device__ constexpr int x_piece_bytes(int nt) { return nt * kBlockK; }
+__host__ __device__ constexpr int x_meta_bytes(int nt) { return 6 * nt * 4; }
+__host__ __device__ constexpr int x_block_bytes(int nt) {
+  return kPieces * x_piece_bytes(nt) + x_meta_bytes(nt);
+}
 
 __device__ __forceinline__ void load_raw(uint32_t* r, const uint2* p) {
   const uint2 v = __ldg(p);
@@ -106,6 +120,82 @@ __device__ constexpr uint32_t w4_idesc(int N) {
   return (1u << 4) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// Splits 8 columns (c8 = column / 8 of the block) of token t; every lane of a
+// warp calls it, eight consecutive lanes holding 64 columns of a token.  v: the
+// values, or NaN or infinities among them: their token's factor becomes NaN, and a
+// NaN sum is formed again without the split.
+__device__ __forceinline__ void split8(uint8_t* block, int nt, int t, int c8, const float (&v)[8],
+                                       bool by32) {
+  float m = 0.f;
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m = fmaxf(m, fabsf(v[i]));
+    finite = finite && isfinite(v[i]);
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const unsigned bad = __ballot_sync(0xffffffffu, !finite);
+  finite = (bad >> (threadIdx.x & 24) & 0xffu) == 0u;
+  // biased exponent of the largest; at least 14, so that the scale stays finite
+  const int ex = max(finite ? static_cast<int>(__float_as_uint(m) >> 23) : 0, 14);
+  const float scale = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(141 - ex)
+  float sum = 0.f;
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = finite ? v[2 * i] * scale : 0.f, hi = finite ? v[2 * i + 1] * scale : 0.f;
+    sum += lo + hi;
+    h[i] = cvt_f16x2(lo, hi);
+  }
+  uint8_t* p = block + t * 128 + ((c8 / 2) ^ (t & 7)) * 16 + c8 % 2 * 8;
+#pragma unroll
+  for (int n = 0; n < kPieces; ++n) {
+    const uint32_t a = __byte_perm(h[0], h[1], 0x7351), b = __byte_perm(h[2], h[3], 0x7351);
+    *reinterpret_cast<uint2*>(p + n * x_piece_bytes(nt)) =
+        make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[q] = sub_f16x2(h[q], h[q] & 0xff00ff00u);
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  if (!by32) sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+  float* meta = reinterpret_cast<float*>(block + kPieces * x_piece_bytes(nt));
+  if (by32 ? c8 % 4 == 0 : c8 % 8 == 0) meta[(by32 ? c8 / 4 : c8 / 8) * nt + t] = 0x1p-9f * sum;
+  if (c8 % 8 == 0)
+    meta[(4 + c8 / 8) * nt + t] =
+        finite ? __uint_as_float(static_cast<uint32_t>(ex - 5) << 23) : __int_as_float(0x7fc00000);
+}
+
+// x, split: a thread block for each block of tokens and of 128 columns, 16 threads a
+// token.  Layer: the tokens of the pairs in sorted_ids.
+__global__ void __launch_bounds__(512)
+    w4_split_kernel(const __nv_bfloat16* __restrict__ x, int T, int K, int nt, int by32,
+                    uint8_t* __restrict__ xq, const int32_t* __restrict__ sorted_ids,
+                    const int32_t* __restrict__ num_padded, int P, int k) {
+  pdl_wait();
+  pdl_trigger();
+  const int n_cols = (K + kBlockK - 1) / kBlockK;
+  const int block = blockIdx.x / n_cols, blk = blockIdx.x % n_cols;
+  if (sorted_ids != nullptr && block * nt >= __ldg(num_padded)) return;
+  const int t = threadIdx.x / 16, c8 = threadIdx.x % 16, col = blk * kBlockK + c8 * 8;
+  long long row = static_cast<long long>(block) * nt + t;
+  bool on;
+  if (sorted_ids != nullptr) {
+    const int pair = __ldg(sorted_ids + row);
+    on = pair < P;
+    row = pair / k;
+  } else {
+    on = row < T;
+  }
+  float v[8];
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (on && col < K) w = __ldg(reinterpret_cast<const uint4*>(x + row * K + col));
+  v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+  v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
+  split8(xq + (static_cast<size_t>(block) * n_cols + blk) * x_block_bytes(nt), nt, t, c8, v, by32);
+}
+
 enum W4Mode { kMatvec, kGateUp, kDown };
 struct W4Job {
   const uint8_t* codes;
@@ -116,10 +206,13 @@ struct W4Job {
   int mode, K;
   int n_rows;    // rows of the result: N, I or H
   int n_blocks;  // blocks of tokens (an upper bound for the layer)
-  const __nv_bfloat16* x;  // tokens, or h by pair (down)
+  const uint8_t* xq;        // x (down: h), split: [token block][column block]
+  const __nv_bfloat16* x;   // tokens (down: h by pair)
   int T;
   void* out;     // matvec: [T][N]; gate/up: h bf16 [pair][I]; down: y fp32 [pair][H]
   int out_fp32;
+  uint8_t* hq;   // gate/up: h, split
+  int h_by32;    // w2's groups are of 32 columns
   int cluster;   // thread blocks that split K
   // layer
   const int32_t* sorted_ids;
@@ -134,22 +227,23 @@ struct W4Job {
 template <int PG, int NT>
 struct W4Shape {
   static constexpr int kN = NT < 16 ? 16 : NT;  // MMA N (16 at least with 128 rows)
+  static constexpr int kSumK = PG == 1 ? 32 : kScaleK;  // columns of one accumulator
   // Columns of a unit, what is multiplied at a time: as many as leave room for
   // two buffers of A and a unit's accumulators in 128 columns of tensor memory.
-  static constexpr bool fits(int unit) { return unit / 2 + kN * (unit / (32 * PG)) <= 128; }
-  static constexpr int kUnitK = fits(128) ? 128 : fits(64) ? 64 : 32;
-  static_assert(fits(kUnitK) && kUnitK % (32 * PG) == 0, "a unit holds whole groups");
+  static constexpr bool fits(int unit) { return unit / 2 + kN * (unit / kSumK) <= 128; }
+  static constexpr int kUnitK = fits(128) ? 128 : 64;
+  static_assert(fits(kUnitK), "tensor memory");
   static constexpr int kUnits = kBlockK / kUnitK;  // of a block of columns
-  static constexpr int kSub = kUnitK / (32 * PG);  // groups of a unit
+  static constexpr int kSub = kUnitK / kSumK;      // accumulators of a unit
   static constexpr int kACols = kUnitK / 4;
   // two sets of accumulators, so that one is read during the next unit's MMAs,
   // where that fits too
   static constexpr int kSums = 2 * kACols + 2 * kN * kSub <= 128 ? 2 : 1;
-  static constexpr int kPieceBytes = NT * kBlockK;       // of x in a block of columns
-  static constexpr int kXBytes = kPieces * kPieceBytes;  // two buffers
-  static constexpr int kPerSm = NT <= 16 ? 4 : NT == 32 ? 3 : 2;
-  static constexpr int kStages = NT == 16 ? 2 : 3;
-  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + 2 * kXBytes + 1024;
+  static constexpr int kStages = 3;
+  static constexpr int kXBytes = kPieces * x_piece_bytes(NT);
+  static constexpr int kPerSm = NT == 8 ? 3 : 2;
+  static constexpr size_t kSmem =
+      1024 + static_cast<size_t>(kStages) * kStageBytes + kXSlots * (kXBytes + x_meta_bytes(NT));
 };
 
 // sum_k x[k] (code[k] - zero) * scale over columns k0 .. k1 of a weight row,
@@ -180,29 +274,25 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     w4_kernel(const __grid_constant__ CUtensorMap map, const W4Job j) {
   using S = W4Shape<PG, NT>;
   constexpr int kStages = S::kStages;
-  constexpr int kBlkGroups = 4 / PG;  // groups of a block of columns
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_full[kStages], s_done[2];  // s_done: even and odd units' MMAs
+  __shared__ uint64_t s_codes[kStages];  // a stage's codes are there
+  __shared__ uint64_t s_x[kXSlots];      // a block of x is there
+  __shared__ uint64_t s_done[2];         // even and odd units' MMAs are done
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_issued;
-  __shared__ unsigned s_bad[2];
-  // of the last three blocks of columns: 2^-9 X by group, and the factor that undoes
-  // the scaling of x and of the codes
-  __shared__ __align__(16) float s_sum[3][kBlkGroups][NT];
-  __shared__ __align__(16) float s_factor[3][NT];
+  __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  uint8_t* s_x = smem + kStages * kStageBytes;
+  uint8_t* x_pieces = smem + kStages * kStageBytes;
+  float* x_meta = reinterpret_cast<float*>(x_pieces + kXSlots * S::kXBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int CS = j.cluster;
   const int rank = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (tid == 0) {
     prefetch_tensormap(&map);
-    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_codes[i], 1);
+    for (int i = 0; i < kXSlots; ++i) mbar_init(&s_x[i], 1);
     mbar_init(&s_done[0], 1);
     mbar_init(&s_done[1], 1);
     s_abort = 0;
-    s_issued = 0;
-    s_bad[0] = s_bad[1] = 0u;
     fence_mbarrier_init();
   }
   pdl_wait();
@@ -222,16 +312,14 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     e = __ldg(j.block_expert + block);
     const int32_t* ids = j.sorted_ids + static_cast<size_t>(block) * NT;
     valid = __popc(__ballot_sync(0xffffffffu, lane < NT && __ldg(ids + min(lane, NT - 1)) < j.P));
-    if (NT > 32) valid += __popc(__ballot_sync(0xffffffffu, __ldg(ids + NT - 32 + lane) < j.P));
   }
-  if (warp == 0) {
+  if (warp == 4) {
     tmem_alloc(&s_tmem, 128);
     tmem_relinquish();
   }
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = s_tmem, t_d = tmem + 2 * S::kACols;
-  const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const size_t expert_row = static_cast<size_t>(e) * j.n_rows * (j.mode == kGateUp ? 2 : 1);
 
   // this block's slice of K, in stages and blocks of columns
@@ -241,251 +329,233 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
   const int n_steps = step1 - step0;
   const int k0 = step0 * kStepK, k1 = min(step1 * kStepK, j.K);
   const int n_blks = (k1 - k0 + kBlockK - 1) / kBlockK;
-
-  auto issue = [&](int step, int slot) {  // one thread
-    uint64_t* bar = &s_full[slot];
-    uint8_t* dst = smem + slot * kStageBytes;
-    mbar_arrive_expect_tx(bar, kStageBytes);
-    s_issued = step + 1;
-    const int col = (step0 + step) * (kStepK / 2), row_a = static_cast<int>(expert_row) + r0;
-    tma_load_2d(dst, &map, bar, col, row_a);
-    tma_load_2d(dst + kStageBytes / 2, &map, bar, col,
-                row_a + (j.mode == kGateUp ? j.n_rows : kRows / 2));
-  };
-  if (warp == 0 && elect_one())
-    for (int i = 0; i < min(kStages, n_steps); ++i) issue(i, i);
-
-  // this thread's weight row (past the result's last one: that one), for its scales
-  const size_t grow = expert_row + min(r0 + tid % rows_out, j.n_rows - 1) +
-                      (j.mode == kGateUp && tid >= rows_out ? j.n_rows : 0);
-  const int groups = (j.K + 32 * PG - 1) / (32 * PG);
-  const size_t group0 = grow * groups + k0 / (32 * PG);
-  // x: columns 8 piece .. of a block of columns of tokens tid / 16, tid / 16 + 8, ..
-  constexpr int kRounds = NT / 8;
-  const int piece = tid % 16;
-  auto token_row = [&](int t) {
-    if (j.mode == kMatvec) return static_cast<size_t>(block) * NT + t;
-    const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
-    return static_cast<size_t>(j.mode == kGateUp ? pair / j.k : pair);
-  };
-  const __nv_bfloat16* xp[kRounds];
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i)
-    xp[i] = j.x + token_row(min(tid / 16 + i * 8, valid - 1)) * j.K + k0 + piece * 8;
-  uint4 x_nx[kRounds];
-  auto fetch_x = [&](int blk) {
-    const bool on = k0 + blk * kBlockK + piece * 8 < k1;
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i)
-      x_nx[i] = on && 2 * warp + i * 8 < valid
-                    ? __ldg(reinterpret_cast<const uint4*>(xp[i] + blk * kBlockK))
-                    : make_uint4(0, 0, 0, 0);
-  };
-  // The pieces of a block of columns of x; its factor and sums go to buffer `at`.
-  auto split_x = [&](int blk, int at) {
-    uint8_t* to = s_x + (blk & 1) * S::kXBytes;
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      if (2 * warp + i * 8 >= valid) break;  // neither of this warp's tokens
-      const int t = tid / 16 + i * 8;
-      uint32_t w[4] = {x_nx[i].x, x_nx[i].y, x_nx[i].z, x_nx[i].w};
-      uint32_t m = max_bf16x2(max_bf16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                              max_bf16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-      m = max_bf16x2(m, m >> 16 | m << 16);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      int ex = static_cast<int>(m >> 7 & 0xffu);  // biased exponent of the largest
-      if (ex == 255) {  // infinite or NaN: the token is summed column by column instead
-        if (piece == 0 && t < valid) atomicOr(&s_bad[t / 32], 1u << (t % 32));
-        ex = 0;
-        w[0] = w[1] = w[2] = w[3] = 0u;
-      }
-      ex = max(ex, 14);  // the scale stays finite
-      const float scale = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(141 - ex)
-      float sum = 0.f;
-      uint32_t h[4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        float lo, hi;
-        unpack2(mul2(pack2(bf16_lo(w[n]), bf16_hi(w[n])), pack2(scale, scale)), lo, hi);
-        sum += lo + hi;
-        h[n] = cvt_f16x2(lo, hi);
-      }
-      // the columns in the order of the spread codes: 0, 2, 4, 6, 1, 3, 5, 7
-      uint8_t* p = to + t * 128 + ((piece / 2) ^ (t & 7)) * 16 + piece % 2 * 8;
-#pragma unroll
-      for (int n = 0; n < kPieces; ++n) {
-        const uint32_t a = __byte_perm(h[0], h[1], 0x7351), b = __byte_perm(h[2], h[3], 0x7351);
-        *reinterpret_cast<uint2*>(p + n * S::kPieceBytes) =
-            make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-        if (n + 1 < kPieces) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) h[q] = sub_f16x2(h[q], h[q] & 0xff00ff00u);
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < 4 * PG; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (piece % (4 * PG) == 0) s_sum[at][piece / (4 * PG)][t] = 0x1p-9f * sum;
-      if (piece == 0) s_factor[at][t] = __uint_as_float(static_cast<uint32_t>(ex - 5) << 23);
-    }
-  };
-  // Scales and zero points of a stage's groups, as they lie in memory: one load
-  // each when every row's stage starts on its size (K a multiple of the stage's
-  // columns), else group by group.
-  constexpr int kGroups = 8 / PG;
-  uint32_t s_raw[kGroups], z_raw[(kGroups + 3) / 4];
-  auto fetch_scales = [&](int step) {
-    const size_t at = group0 + static_cast<size_t>(step) * kGroups;
-    if (step >= n_steps) return;
-    if (j.whole_stages) {
-      if (j.scale_bf16) {
-        const uint8_t* p = static_cast<const uint8_t*>(j.scales) + at * 2;
-        if (PG == 4) s_raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-        if (PG == 2) load_raw(s_raw, reinterpret_cast<const uint2*>(p));
-        if (PG == 1) load_raw(s_raw, reinterpret_cast<const uint4*>(p));
-      } else {
-        const uint8_t* p = static_cast<const uint8_t*>(j.scales) + at * 4;
-        if (PG == 4) load_raw(s_raw, reinterpret_cast<const uint2*>(p));
-        if (PG <= 2) load_raw(s_raw, reinterpret_cast<const uint4*>(p));
-        if (PG == 1) load_raw(s_raw + 4, reinterpret_cast<const uint4*>(p) + 1);
-      }
-      if (ZP) {
-        if (PG == 4) z_raw[0] = __ldg(reinterpret_cast<const uint16_t*>(j.zeros + at));
-        if (PG == 2) z_raw[0] = __ldg(reinterpret_cast<const uint32_t*>(j.zeros + at));
-        if (PG == 1) load_raw(z_raw, reinterpret_cast<const uint2*>(j.zeros + at));
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const bool on = k0 + (step * kGroups + i) * (32 * PG) < k1;
-      if (j.scale_bf16) {
-        const uint32_t v = on ? __ldg(static_cast<const uint16_t*>(j.scales) + at + i) : 0;
-        s_raw[i / 2] = i % 2 ? s_raw[i / 2] | v << 16 : v;
-      } else {
-        s_raw[i] = on ? __ldg(static_cast<const uint32_t*>(j.scales) + at + i) : 0;
-      }
-      if (ZP) {
-        const uint32_t v = on ? __ldg(j.zeros + at + i) : 0;
-        z_raw[i / 4] = i % 4 ? z_raw[i / 4] | v << (8 * (i % 4)) : v;
-      }
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < (kGroups + 3) / 4; ++i) z_raw[i] = 0;
-  fetch_scales(0);
-  fetch_x(0);
+  // this thread's weight row (past the result's last one: that one)
+  const int row = tid % kRows;
+  const size_t grow = expert_row + min(r0 + row % rows_out, j.n_rows - 1) +
+                      (j.mode == kGateUp && row >= rows_out ? j.n_rows : 0);
 
   float acc[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) acc[t] = 0.f;
-  bool ok = true;  // once a wait gives up, the loop runs out without waits and MMAs
-  float s_step[kGroups], s_old[S::kSub], z_old[S::kSub];
-  uint32_t z_step[(kGroups + 3) / 4];
-  int x_at = 0, x_old = 0;  // buffers of the sums of x: this unit's, the last one's
-  // adds unit u's sums, scaled; h: its place in its block of columns
-  auto flush = [&](int u, int h) {
-    ok = ok && wait(&s_done[u & 1], u >> 1 & 1, &s_abort, j.timeout_ns);
-    tc_fence_after_sync();
-    const uint32_t at = t_d + lanes + (S::kSums == 2 ? (u & 1) * (S::kN * S::kSub) : 0);
-#pragma unroll
-    for (int i = 0; i < S::kSub; ++i) {
-      const uint64_t zz = pack2(-z_old[i], -z_old[i]), ss = pack2(s_old[i], s_old[i]);
-      const float* sum = s_sum[x_old][h * S::kSub + i];
-#pragma unroll
-      for (int t0 = 0; t0 < NT; t0 += 8) {
-        uint32_t d[8];
-        tmem_ld8_async(at + i * S::kN + t0, d);
-        float4 xs[2], f[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          xs[n] = *reinterpret_cast<const float4*>(sum + t0 + 4 * n);
-          f[n] = *reinterpret_cast<const float4*>(s_factor[x_old] + t0 + 4 * n);
-        }
-        tmem_wait_ld8(d);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float4 xv = xs[n / 2], fv = f[n / 2];
-          const uint64_t x2 = n % 2 ? pack2(xv.z, xv.w) : pack2(xv.x, xv.y);
-          const uint64_t f2 = n % 2 ? pack2(fv.z, fv.w) : pack2(fv.x, fv.y);
-          const uint64_t d2 = pack2(__uint_as_float(d[2 * n]), __uint_as_float(d[2 * n + 1]));
-          unpack2(fma2(ss, mul2(f2, fma2(zz, x2, d2)), pack2(acc[t0 + 2 * n], acc[t0 + 2 * n + 1])),
-                  acc[t0 + 2 * n], acc[t0 + 2 * n + 1]);
-        }
-      }
-    }
-  };
-  // a block of 128 columns, the hb-th of its stage
-  auto columns = [&](int blk, int step, int slot, auto which) {
-    constexpr int hb = decltype(which)::value;
-    const uint8_t* codes = smem + slot * kStageBytes + tid * 128;
-#pragma unroll
-    for (int h = 0; h < S::kUnits; ++h) {
-      const int u = blk * S::kUnits + h;
-      uint32_t v[S::kACols];
-#pragma unroll
-      for (int c = 0; c < S::kUnitK / 32; ++c) {
-        const uint4 q = *reinterpret_cast<const uint4*>(
-            codes + ((hb * 4 + h * (S::kUnitK / 32) + c) ^ (tid & 7)) * 16);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          v[c * 8 + 2 * n] = w[n] & 0x0f0f0f0fu;
-          v[c * 8 + 2 * n + 1] = w[n] >> 4 & 0x0f0f0f0fu;
-        }
-      }
-      // the MMAs that read this buffer of A, and of x, were waited for when their
-      // sums were added
-      const uint32_t a = tmem + (u & 1) * S::kACols;
-      if (S::kACols == 8) {
-        tmem_st8(a + lanes, v);
+  bool ok = true;  // once a wait gives up, the loops run out without waits and MMAs
+
+  if (warp == 4) {
+    // ---------------------------------------------------------- copies and MMAs
+    auto issue_codes = [&](int step) {
+      uint64_t* bar = &s_codes[step % kStages];
+      uint8_t* dst = smem + step % kStages * kStageBytes;
+      mbar_arrive_expect_tx(bar, kStageBytes);
+      const int col = (step0 + step) * (kStepK / 2), row_a = static_cast<int>(expert_row) + r0;
+      tma_load_2d(dst, &map, bar, col, row_a);
+      tma_load_2d(dst + kStageBytes / 2, &map, bar, col,
+                  row_a + (j.mode == kGateUp ? j.n_rows : kRows / 2));
+    };
+    const int x_rows = (valid + 7) / 8 * 8;
+    const uint8_t* xq =
+        j.xq + (static_cast<size_t>(block) * ((j.K + kBlockK - 1) / kBlockK) + k0 / kBlockK) *
+                   x_block_bytes(NT);
+    auto issue_x = [&](int blk) {
+      const int slot = blk % kXSlots;
+      uint64_t* bar = &s_x[slot];
+      uint8_t* dst = x_pieces + slot * S::kXBytes;
+      const uint8_t* src = xq + static_cast<size_t>(blk) * x_block_bytes(NT);
+      mbar_arrive_expect_tx(bar, kPieces * x_rows * 128 + x_meta_bytes(NT));
+      if (x_rows == NT) {
+        bulk_load(dst, src, S::kXBytes, bar);
       } else {
+        for (int n = 0; n < kPieces; ++n)
+          bulk_load(dst + n * x_piece_bytes(NT), src + n * x_piece_bytes(NT), x_rows * 128, bar);
+      }
+      bulk_load(x_meta + slot * (x_meta_bytes(NT) / 4), src + S::kXBytes, x_meta_bytes(NT), bar);
+    };
+    int codes_issued = min(kStages, n_steps), x_issued = min(kXSlots, n_blks);
+    if (elect_one()) {
+      for (int i = 0; i < codes_issued; ++i) issue_codes(i);
+      for (int i = 0; i < x_issued; ++i) issue_x(i);
+    }
+    __syncwarp();
+    // N: the block's tokens, and eight stand for both eight-row halves of 16
+    const uint32_t idesc = w4_idesc(max(16, (valid + 15) / 16 * 16));
+    const uint64_t db0 = sdesc_kmajor_sw128(smem_addr(x_pieces)) -
+                         (NT == 8 ? static_cast<uint64_t>(1024 >> 4) << 32 : 0);
+    for (int blk = 0; blk < n_blks; ++blk) {
+      const bool there = ok && wait(&s_x[blk % kXSlots], blk / kXSlots & 1, &s_abort, j.timeout_ns);
+      ok = __all_sync(0xffffffffu, there);
 #pragma unroll
-        for (int n = 0; n < S::kACols; n += 16) tmem_st16(a + lanes + n, v + n);
-      }
-      if (h == 0) {
-        split_x(blk, x_at);
-        fetch_x(blk + 1);
-        fence_proxy_async_smem();
-      }
-      if (S::kSums == 1 && u > 0) flush(u - 1, (h + S::kUnits - 1) % S::kUnits);
-      tmem_wait_st();
-      tc_fence_before_sync();
-      __syncthreads();  // A and x are in place, and the unit's codes are read
-      if (warp == 0 && elect_one()) {
-        tc_fence_after_sync();
-        if (ok) {
-          const uint64_t db = sdesc_kmajor_sw128(smem_addr(s_x)) + (blk & 1) * (S::kXBytes / 16) -
-                              // eight tokens stand for both eight-row halves of N
-                              (NT == 8 ? static_cast<uint64_t>(1024 >> 4) << 32 : 0);
+      for (int h = 0; h < S::kUnits; ++h) {
+        const int u = blk * S::kUnits + h;
+        named_barrier(1 + (u & 1), kThreads);  // A is in place
+        if (ok && elect_one()) {
+          tc_fence_after_sync();
+          const uint64_t db = db0 + blk % kXSlots * (S::kXBytes / 16);
+          const uint32_t a = tmem + (u & 1) * S::kACols;
           const uint32_t d = t_d + (S::kSums == 2 ? (u & 1) * (S::kN * S::kSub) : 0);
 #pragma unroll
           for (int n = kPieces - 1; n >= 0; --n)  // small pieces first
 #pragma unroll
             for (int i = 0; i < S::kUnitK / 32; ++i)
-              umma_f8_ts(d + i / PG * S::kN, a + i * 8,
-                         db + n * (S::kPieceBytes / 16) + (h * (S::kUnitK / 32) + i) * 2,
-                         w4_idesc(S::kN), n < kPieces - 1 || i % PG != 0);
+              umma_f8_ts(d + i / (S::kSumK / 32) * S::kN, a + i * 8,
+                         db + n * (x_piece_bytes(NT) / 16) + (h * (S::kUnitK / 32) + i) * 2, idesc,
+                         n < kPieces - 1 || i % (S::kSumK / 32) != 0);
           umma_commit(&s_done[u & 1]);
-          // the stage is free after its second block
-          if (hb == 1 && h == S::kUnits - 1 && step + kStages < n_steps)
-            issue(step + kStages, slot);
+        }
+        __syncwarp();
+      }
+      // Every warp has read the block's codes, and has added the sums of the block
+      // before the last: a stage is free after its second block, and x's buffer of
+      // two blocks ago too.
+      if (ok && elect_one()) {
+        if (blk % 2 == 1 && codes_issued < n_steps) issue_codes(codes_issued);
+        if (blk >= 2 && x_issued < n_blks) issue_x(x_issued);
+      }
+      __syncwarp();
+      if (blk % 2 == 1 && codes_issued < n_steps) ++codes_issued;
+      if (blk >= 2 && x_issued < n_blks) ++x_issued;
+    }
+    if (!ok && lane == 0) {  // the copies in flight land before the block leaves
+      volatile int never = 0;
+      for (int i = max(0, codes_issued - kStages); i < codes_issued; ++i)
+        mbar_wait(&s_codes[i % kStages], i / kStages & 1, &never, kDrainNs);
+      for (int i = max(0, x_issued - kXSlots); i < x_issued; ++i)
+        mbar_wait(&s_x[i % kXSlots], i / kXSlots & 1, &never, kDrainNs);
+    }
+  } else {
+    // ---------------------------------------------------------- codes and sums
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int groups = (j.K + 32 * PG - 1) / (32 * PG);
+    const size_t group0 = grow * groups + k0 / (32 * PG);
+    // Scales and zero points of a stage's groups, as they lie in memory: one load
+    // each when every row's stage starts on its size (K a multiple of the stage's
+    // columns), else group by group.
+    constexpr int kGroups = 8 / PG;
+    uint32_t s_raw[kGroups], z_raw[(kGroups + 3) / 4];
+    auto fetch_scales = [&](int step) {
+      const size_t at = group0 + static_cast<size_t>(step) * kGroups;
+      if (step >= n_steps) return;
+      if (j.whole_stages) {
+        if (j.scale_bf16) {
+          const uint8_t* p = static_cast<const uint8_t*>(j.scales) + at * 2;
+          if (PG == 4) s_raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          if (PG == 2) load_raw(s_raw, reinterpret_cast<const uint2*>(p));
+          if (PG == 1) load_raw(s_raw, reinterpret_cast<const uint4*>(p));
+        } else {
+          const uint8_t* p = static_cast<const uint8_t*>(j.scales) + at * 4;
+          if (PG == 4) load_raw(s_raw, reinterpret_cast<const uint2*>(p));
+          if (PG <= 2) load_raw(s_raw, reinterpret_cast<const uint4*>(p));
+          if (PG == 1) load_raw(s_raw + 4, reinterpret_cast<const uint4*>(p) + 1);
+        }
+        if (ZP) {
+          if (PG == 4) z_raw[0] = __ldg(reinterpret_cast<const uint16_t*>(j.zeros + at));
+          if (PG == 2) z_raw[0] = __ldg(reinterpret_cast<const uint32_t*>(j.zeros + at));
+          if (PG == 1) load_raw(z_raw, reinterpret_cast<const uint2*>(j.zeros + at));
+        }
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const bool on = k0 + (step * kGroups + i) * (32 * PG) < k1;
+        if (j.scale_bf16) {
+          const uint32_t v = on ? __ldg(static_cast<const uint16_t*>(j.scales) + at + i) : 0;
+          s_raw[i / 2] = i % 2 ? s_raw[i / 2] | v << 16 : v;
+        } else {
+          s_raw[i] = on ? __ldg(static_cast<const uint32_t*>(j.scales) + at + i) : 0;
+        }
+        if (ZP) {
+          const uint32_t v = on ? __ldg(j.zeros + at + i) : 0;
+          z_raw[i / 4] = i % 4 ? z_raw[i / 4] | v << (8 * (i % 4)) : v;
         }
       }
-      if (S::kSums == 2 && u > 0) flush(u - 1, (h + S::kUnits - 1) % S::kUnits);
+    };
+#pragma unroll
+    for (int i = 0; i < (kGroups + 3) / 4; ++i) z_raw[i] = 0;
+    fetch_scales(0);
+    // scales of the blocks of a stage by accumulator
+    constexpr int kBlkSums = kBlockK / S::kSumK;
+    float s_step[kGroups], s_old[S::kSub], z_old[S::kSub];
+    uint32_t z_step[(kGroups + 3) / 4];
+    // adds unit u's sums, scaled; h: its place in block of columns blk
+    auto flush = [&](int u, int blk, int h) {
+      const bool there =
+          ok && wait(&s_done[u & 1], u >> 1 & 1, &s_abort, j.timeout_ns) &&
+          wait(&s_x[blk % kXSlots], blk / kXSlots & 1, &s_abort, j.timeout_ns);
+      ok = __all_sync(0xffffffffu, there);
+      tc_fence_after_sync();
+      const uint32_t at = t_d + lanes + (S::kSums == 2 ? (u & 1) * (S::kN * S::kSub) : 0);
+      const float* meta = x_meta + blk % kXSlots * (x_meta_bytes(NT) / 4);
 #pragma unroll
       for (int i = 0; i < S::kSub; ++i) {
-        const int g = hb * kBlkGroups + h * S::kSub + i;
-        s_old[i] = s_step[g];
-        z_old[i] = ZP ? static_cast<float>(z_step[g / 4] >> (8 * (g % 4)) & 0xffu) : 8.f;
+        const uint64_t zz = pack2(-z_old[i], -z_old[i]), ss = pack2(s_old[i], s_old[i]);
+        const float* sum = meta + (h * S::kSub + i) * NT;
+        const float* factor = meta + (4 + (h * S::kSub + i) * S::kSumK / kScaleK) * NT;
+#pragma unroll
+        for (int t0 = 0; t0 < NT; t0 += 8) {
+          if (t0 > 0 && t0 >= valid) break;
+          uint32_t d[8];
+          tmem_ld8_async(at + i * S::kN + t0, d);
+          float4 xs[2], f[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            xs[n] = *reinterpret_cast<const float4*>(sum + t0 + 4 * n);
+            f[n] = *reinterpret_cast<const float4*>(factor + t0 + 4 * n);
+          }
+          tmem_wait_ld8(d);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float4 xv = xs[n / 2], fv = f[n / 2];
+            const uint64_t x2 = n % 2 ? pack2(xv.z, xv.w) : pack2(xv.x, xv.y);
+            const uint64_t f2 = n % 2 ? pack2(fv.z, fv.w) : pack2(fv.x, fv.y);
+            const uint64_t d2 = pack2(__uint_as_float(d[2 * n]), __uint_as_float(d[2 * n + 1]));
+            float& lo = acc[t0 + 2 * n];
+            float& hi = acc[t0 + 2 * n + 1];
+            unpack2(fma2(ss, mul2(f2, fma2(zz, x2, d2)), pack2(lo, hi)), lo, hi);
+          }
+        }
       }
-      x_old = x_at;
-    }
-    x_at = x_at == 2 ? 0 : x_at + 1;
-  };
-  int slot = 0, phase = 0;
-  for (int step = 0; step < n_steps; ++step) {
-    ok = ok && wait(&s_full[slot], phase, &s_abort, j.timeout_ns);
+    };
+    // a block of 128 columns, the hb-th of its stage
+    auto columns = [&](int blk, int slot, auto which) {
+      constexpr int hb = decltype(which)::value;
+      const uint8_t* codes = smem + slot * kStageBytes + tid * 128;
+#pragma unroll
+      for (int h = 0; h < S::kUnits; ++h) {
+        const int u = blk * S::kUnits + h;
+        uint32_t v[S::kACols];
+#pragma unroll
+        for (int c = 0; c < S::kUnitK / 32; ++c) {
+          const uint4 q = *reinterpret_cast<const uint4*>(
+              codes + ((hb * 4 + h * (S::kUnitK / 32) + c) ^ (tid & 7)) * 16);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            v[c * 8 + 2 * n] = w[n] & 0x0f0f0f0fu;
+            v[c * 8 + 2 * n + 1] = w[n] >> 4 & 0x0f0f0f0fu;
+          }
+        }
+        // the MMAs that read this buffer of A were waited for when their sums were added
+        const uint32_t a = tmem + (u & 1) * S::kACols + lanes;
+#pragma unroll
+        for (int n = 0; n < S::kACols; n += 16) tmem_st16(a + n, v + n);
+        const int prev_blk = h == 0 ? blk - 1 : blk, prev_h = (h + S::kUnits - 1) % S::kUnits;
+        if (S::kSums == 1 && u > 0) flush(u - 1, prev_blk, prev_h);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        // A is in place, and the unit's codes are read.  (After a wait that gave up
+        // nothing but this barrier keeps the warps together.)
+        if (ok) named_barrier_arrive(1 + (u & 1), kThreads);
+        else named_barrier(1 + (u & 1), kThreads);
+        if (S::kSums == 2 && u > 0) flush(u - 1, prev_blk, prev_h);
+#pragma unroll
+        for (int i = 0; i < S::kSub; ++i) {
+          const int g = (hb * kBlkSums + h * S::kSub + i) * S::kSumK / (32 * PG);
+          s_old[i] = s_step[g];
+          z_old[i] = ZP ? static_cast<float>(z_step[g / 4] >> (8 * (g % 4)) & 0xffu) : 8.f;
+        }
+      }
+    };
+    int slot = 0, phase = 0;
+    for (int step = 0; step < n_steps; ++step) {
+      const bool there = ok && wait(&s_codes[slot], phase, &s_abort, j.timeout_ns);
+      ok = __all_sync(0xffffffffu, there);
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
         s_step[i] = __uint_as_float(!j.scale_bf16 ? s_raw[i]
@@ -493,73 +563,103 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
                                                   : s_raw[i / 2] << 16);
 #pragma unroll
       for (int i = 0; i < (kGroups + 3) / 4; ++i) z_step[i] = z_raw[i];
-    fetch_scales(step + 1);
-    columns(2 * step, step, slot, std::integral_constant<int, 0>{});
-    if (2 * step + 1 < n_blks) columns(2 * step + 1, step, slot, std::integral_constant<int, 1>{});
-    if (++slot == kStages) slot = 0, phase ^= 1;
+      fetch_scales(step + 1);
+      columns(2 * step, slot, std::integral_constant<int, 0>{});
+      if (2 * step + 1 < n_blks) columns(2 * step + 1, slot, std::integral_constant<int, 1>{});
+      if (++slot == kStages) slot = 0, phase ^= 1;
+    }
+    flush(n_blks * S::kUnits - 1, n_blks - 1, S::kUnits - 1);
+    // a sum that is not a number: as the weights and tokens have it, column by column
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t < valid && isnan(acc[t])) {
+        size_t at = static_cast<size_t>(block) * NT + t;
+        if (j.mode != kMatvec) {
+          const int pair = __ldg(j.sorted_ids + at);
+          at = static_cast<size_t>(j.mode == kGateUp ? pair / j.k : pair);
+        }
+        acc[t] = w4_row_plain(j, 32 * PG, grow, j.x + at * j.K, k0, k1);
+      }
+    }
   }
-  flush(n_blks * S::kUnits - 1, S::kUnits - 1);
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (s_bad[0] | s_bad[1]) {
-#pragma unroll 1
-    for (int t = 0; t < valid; ++t) {
-      if (!(s_bad[t / 32] >> (t % 32) & 1u)) continue;
-      const float v = w4_row_plain(j, 32 * PG, grow, j.x + token_row(t) * j.K, k0, k1);
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-        if (i == t) acc[i] = v;
-    }
-  }
   if (s_abort) {
-    if (tid == 0) {  // the copies in flight land before the block leaves
-      if (j.err != nullptr) atomicOr(j.err, kDevErrTimeout);
-      volatile int never = 0;
-      for (int i = max(0, s_issued - kStages); i < s_issued; ++i)
-        mbar_wait(&s_full[i % kStages], i / kStages & 1, &never, kDrainNs);
-    }
+    if (tid == 0 && j.err != nullptr) atomicOr(j.err, kDevErrTimeout);
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = __int_as_float(0x7fc00000);  // a wrong sum shows
-    __syncthreads();
   }
-  if (warp == 0) {
+  if (warp == 4) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 128);
   }
   // the sums over the cluster's slices of K, in rank order, in the stages' space:
   // red[token][row]
   float* red = reinterpret_cast<float*>(smem);
+  if (warp < 4) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) red[t * kRows + tid] = acc[t];
+    for (int t = 0; t < NT; ++t) red[t * kRows + tid] = acc[t];
+  }
   __syncwarp();
   if (CS > 1) cluster_sync();
   else __syncthreads();
   const uint32_t red_at = smem_addr(red);
-  auto sum = [&](int t, int row) {
-    if (CS == 1) return red[t * kRows + row];
+  auto sum = [&](int t, int r) {
+    if (CS == 1) return red[t * kRows + r];
     float v = 0.f;
     for (int i = 0; i < CS; ++i)
-      v += ld_cluster_f32(mapa_shared(red_at + (t * kRows + row) * 4, i));
+      v += ld_cluster_f32(mapa_shared(red_at + (t * kRows + r) * 4, i));
     return v;
   };
-  for (int i = rank * kThreads + tid; i < rows_out * valid; i += CS * kThreads) {
-    const int t = i / rows_out, r = i % rows_out;
-    if (r0 + r >= j.n_rows) continue;
-    if (j.mode == kMatvec) {
+  if (j.mode == kGateUp) {
+    // h of this rank's tokens (rank, rank + CS, ..), kept in bf16 and split
+    float* hs = red + NT * kRows;  // [token][64]
+    const int mine = rank < valid ? (valid - rank + CS - 1) / CS : 0;
+    for (int i = tid; i < mine * rows_out; i += kThreads) {
+      const int t = rank + i / rows_out * CS, r = i % rows_out;
+      float h = 0.f;
+      if (r0 + r < j.n_rows) {
+        const float gate = sum(t, r), up = sum(t, r + rows_out);
+        const __nv_bfloat16 b = __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
+        const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
+        static_cast<__nv_bfloat16*>(j.out)[static_cast<size_t>(pair) * j.n_rows + r0 + r] = b;
+        h = __bfloat162float(b);
+      }
+      hs[i] = h;
+    }
+    __syncthreads();
+    const int n_cols = (j.n_rows + kBlockK - 1) / kBlockK;
+    uint8_t* to = j.hq + (static_cast<size_t>(block) * n_cols + r0 / kBlockK) * x_block_bytes(NT);
+    // eight threads a token; the last rows of h also stand for the block's other
+    // half, zeros, where no thread block has it
+    const bool both = r0 % kBlockK == 0 && r0 + rows_out >= j.n_rows;
+    for (int i0 = 0; i0 < mine * 8; i0 += kThreads) {
+      const int i = i0 + tid, ti = min(i / 8, max(mine - 1, 0)), c = i % 8;
+      const int t = rank + ti * CS;
+      float v[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) v[n] = hs[ti * rows_out + c * 8 + n];
+      split8(to, NT, t, r0 % kBlockK / 8 + c, v, j.h_by32);
+      if (both) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) v[n] = 0.f;
+        split8(to, NT, t, 8 + c, v, j.h_by32);
+      }
+    }
+  } else {
+    for (int i = rank * kThreads + tid; i < rows_out * valid; i += CS * kThreads) {
+      const int t = i / rows_out, r = i % rows_out;
+      if (r0 + r >= j.n_rows) continue;
       const float v = sum(t, r);
-      const size_t o = (static_cast<size_t>(block) * NT + t) * j.n_rows + r0 + r;
-      if (j.out_fp32) static_cast<float*>(j.out)[o] = v;
-      else static_cast<__nv_bfloat16*>(j.out)[o] = __float2bfloat16_rn(v);
-    } else {
-      const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
-      const size_t o = static_cast<size_t>(pair) * j.n_rows + r0 + r;
-      if (j.mode == kGateUp) {
-        const float gate = sum(t, r), up = sum(t, r + kRows / 2);
-        static_cast<__nv_bfloat16*>(j.out)[o] =
-            __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
+      if (j.mode == kMatvec) {
+        const size_t o = (static_cast<size_t>(block) * NT + t) * j.n_rows + r0 + r;
+        if (j.out_fp32) static_cast<float*>(j.out)[o] = v;
+        else static_cast<__nv_bfloat16*>(j.out)[o] = __float2bfloat16_rn(v);
       } else {
-        static_cast<float*>(j.out)[o] = __ldg(j.wts + pair) * sum(t, r);
+        const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
+        static_cast<float*>(j.out)[static_cast<size_t>(pair) * j.n_rows + r0 + r] =
+            __ldg(j.wts + pair) * v;
       }
     }
   }
@@ -604,6 +704,11 @@ cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaSt
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(S::kSmem)),
                           "smem attribute");
+  if (e == cudaSuccess)
+    e = checked(cudaFuncSetAttribute(w4_kernel<PG, ZP, NT>,
+                                     cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared),
+                "smem attribute");
   if (e != cudaSuccess) return e;
   W4Job j = job;
   j.whole_stages = j.K % kStepK == 0 && reinterpret_cast<uintptr_t>(j.scales) % 16 == 0 &&
@@ -632,8 +737,7 @@ cudaError_t launch_tokens(const CUtensorMap& map, const W4Job& j, int nt, int nu
                           cudaStream_t st) {
   if (nt == 8) return launch<PG, ZP, 8>(map, j, num_sms, st);
   if (nt == 16) return launch<PG, ZP, 16>(map, j, num_sms, st);
-  if (nt == 32) return launch<PG, ZP, 32>(map, j, num_sms, st);
-  return launch<PG, ZP, 64>(map, j, num_sms, st);
+  return launch<PG, ZP, 32>(map, j, num_sms, st);
 }
 
 cudaError_t launch_job(const CUtensorMap& map, int group, const W4Job& j, int nt, int num_sms,
@@ -656,10 +760,14 @@ void set_weight(W4Job& j, const W4View& w) {
 
 }  // namespace
 
-int w4_block_rows(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+int w4_block_rows(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : 32; }
+
+size_t w4_split_bytes(long long blocks, int nt, int K) {
+  return static_cast<size_t>(blocks) * ((K + kBlockK - 1) / kBlockK) * x_block_bytes(nt);
+}
 
 cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int T, int K, int N,
-                             const W4View& w, void* out, bool out_fp32,
+                             const W4View& w, void* out, bool out_fp32, uint8_t* scratch,
                              unsigned long long timeout_ns, int num_sms, cudaStream_t st) {
   const int nt = w4_block_rows(T);
   W4Job j{};
@@ -668,11 +776,18 @@ cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int
   j.K = K;
   j.n_rows = N;
   j.n_blocks = (T + nt - 1) / nt;
+  j.xq = scratch;
   j.x = x;
   j.T = T;
   j.out = out;
   j.out_fp32 = out_fp32 ? 1 : 0;
   j.timeout_ns = timeout_ns;
+  const int n_cols = (K + kBlockK - 1) / kBlockK;
+  const cudaError_t e =
+      launch_pdl(w4_split_kernel, dim3(static_cast<unsigned>(j.n_blocks * n_cols)), dim3(nt * 16),
+                 0, st, x, T, K, nt, w.group == 32 ? 1 : 0, scratch,
+                 static_cast<const int32_t*>(nullptr), static_cast<const int32_t*>(nullptr), 0, 1);
+  if (e != cudaSuccess) return e;
   return launch_job(map, w.group, j, nt, num_sms, st);
 }
 
@@ -686,9 +801,12 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   j.K = p.H;
   j.n_rows = p.I;
   j.n_blocks = static_cast<int>(std::min(P, (P + std::min<long long>(p.E, P) * (nt - 1)) / nt));
+  j.xq = p.xq;
   j.x = p.x;
   j.T = p.T;
   j.out = p.h;
+  j.hq = p.hq;
+  j.h_by32 = p.w2.group == 32 ? 1 : 0;
   j.sorted_ids = p.sorted_ids;
   j.block_expert = p.block_expert;
   j.num_padded = p.num_padded;
@@ -697,12 +815,19 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   j.k = p.k;
   j.err = p.err;
   j.timeout_ns = p.timeout_ns;
-  cudaError_t e = launch_job(map13, p.w13.group, j, nt, num_sms, st);
+  const int n_cols = (p.H + kBlockK - 1) / kBlockK;
+  cudaError_t e = launch_pdl(
+      w4_split_kernel, dim3(static_cast<unsigned>(j.n_blocks * n_cols)), dim3(nt * 16), 0, st, p.x,
+      p.T, p.H, nt, p.w13.group == 32 ? 1 : 0, p.xq, p.sorted_ids, p.num_padded,
+      static_cast<int>(P), p.k);
+  if (e != cudaSuccess) return e;
+  e = launch_job(map13, p.w13.group, j, nt, num_sms, st);
   if (e != cudaSuccess) return e;
   set_weight(j, p.w2);
   j.mode = kDown;
   j.K = p.I;
   j.n_rows = p.H;
+  j.xq = p.hq;
   j.x = p.h;
   j.out = p.y;
   e = launch_job(map2, p.w2.group, j, nt, num_sms, st);

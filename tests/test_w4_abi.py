@@ -33,7 +33,7 @@ def test_workspace_size(lib):
 
 def test_launch_count(lib):
     assert moe.moe_w4_launch_count(0, 2048, 768, 128, 8) == 0
-    assert 1 <= moe.moe_w4_launch_count(1, 2048, 768, 128, 8) <= 5
+    assert 1 <= moe.moe_w4_launch_count(1, 2048, 768, 128, 8) <= 6
     assert moe.moe_w4_launch_count(1, 2040, 768, 128, 8) == -1
     assert moe.moe_w4_launch_count(1, 2048, 700, 128, 8) == -1
     assert moe.moe_w4_launch_count(1, 2048, 768, 128, 129) == -1
@@ -53,13 +53,23 @@ def test_matvec_refusals(lib, kw, w, code):
     a = dict(x=16, T=2, K=64, N=8, out=16, dtype=FP32)
     a.update(kw)
     st = lib.moe_w4_matvec(ctypes.c_void_p(a["x"]), a["T"], a["K"], a["N"],
-                           ctypes.byref(weight(**w)), ctypes.c_void_p(a["out"]), a["dtype"], None)
+                           ctypes.byref(weight(**w)), ctypes.c_void_p(a["out"]), a["dtype"],
+                           ctypes.c_void_p(16), 1 << 40, None)
     assert st == code
 
 
 def test_matvec_null_weight(lib):
     assert lib.moe_w4_matvec(ctypes.c_void_p(16), 1, 32, 1, None, ctypes.c_void_p(16), FP32,
-                             None) == 1
+                             ctypes.c_void_p(16), 1 << 40, None) == 1
+
+
+def test_matvec_scratch(lib):
+    need = moe.moe_w4_matvec_scratch_size(5, 96)
+    assert 0 < need < moe.moe_w4_matvec_scratch_size(9, 96)
+    assert moe.moe_w4_matvec_scratch_size(0, 96) == 0
+    for ptr, size in ((None, need), (8, need), (16, need - 1)):
+        assert lib.moe_w4_matvec(ctypes.c_void_p(16), 5, 96, 3, ctypes.byref(weight()),
+                                 ctypes.c_void_p(16), FP32, ctypes.c_void_p(ptr), size, None) == 3
 
 
 def layer_args(**kw):
