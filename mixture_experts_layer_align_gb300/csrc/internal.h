@@ -176,8 +176,8 @@ struct W4View {
 };
 // map: the codes as bytes [rows][K/2], boxes of 128 bytes x 64 rows, 128-byte swizzle.
 cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int T, int K, int N,
-                             const W4View& w, void* out, bool out_fp32, uint8_t* scratch,
-                             unsigned long long timeout_ns, int num_sms, cudaStream_t st);
+                             const W4View& w, void* out, bool out_fp32, uint8_t* scratch, int num_sms,
+                             cudaStream_t st);
 // Bytes of `blocks` blocks of nt tokens with K columns, split (16-byte aligned).
 size_t w4_split_bytes(long long blocks, int nt, int K);
 struct W4LayerParams {
@@ -193,10 +193,10 @@ struct W4LayerParams {
   float* y;                     // [T*k][H]
   __nv_bfloat16* out;
   int* err;                     // status word
-  unsigned long long timeout_ns;
 };
 // Rows of an alignment block: the pairs of one expert that one thread block takes.
-int w4_block_rows(int T);
+int w4_block_rows(int T);                       // matvec
+int w4_layer_block_rows(int T, int E, int k);   // layer
 cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
                             const W4LayerParams& p, int num_sms, cudaStream_t st);
 

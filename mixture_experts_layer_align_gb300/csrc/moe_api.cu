@@ -740,7 +740,7 @@ struct W4Layout {
 
 W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
   W4Layout L;
-  const int bm = w4_block_rows(T);
+  const int bm = w4_layer_block_rows(T, E, k);
   const size_t P = static_cast<size_t>(T) * k;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -852,8 +852,8 @@ moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tens
   CUtensorMap map;
   if (!make_tmap(&map, w->codes, false, K / 2, N, 64)) return MOE_ERR_CUDA;
   return launch_w4_matvec(map, static_cast<const __nv_bfloat16*>(x), T, K, N, w4_view(*w), out,
-                          out_dtype == MOE_DT_FP32, static_cast<uint8_t*>(scratch), kWaitLimitNs,
-                          dev.num_sms, stream) == cudaSuccess
+                          out_dtype == MOE_DT_FP32, static_cast<uint8_t*>(scratch), dev.num_sms,
+                          stream) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -906,7 +906,7 @@ moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t worksp
   ap.ids = ids;
   ap.P = T * k;
   ap.E = E;
-  ap.bm = w4_block_rows(T);
+  ap.bm = w4_layer_block_rows(T, E, k);
   ap.chunk = align_chunk();
   ap.counts = a->counts_out ? a->counts_out : reinterpret_cast<int32_t*>(ws + L.counts);
   ap.offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
@@ -924,7 +924,6 @@ moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t worksp
   p.y = reinterpret_cast<float*>(ws + L.y);
   p.out = static_cast<__nv_bfloat16*>(a->out);
   p.err = &reinterpret_cast<Ctrl*>(ws + L.ctrl)->err;
-  p.timeout_ns = kWaitLimitNs;
   CUtensorMap map13, map2;
   if (!make_tmap(&map13, a->w13.codes, false, H / 2, static_cast<uint64_t>(E) * 2 * I, 64) ||
       !make_tmap(&map2, a->w2.codes, false, I / 2, static_cast<uint64_t>(E) * H, 64))

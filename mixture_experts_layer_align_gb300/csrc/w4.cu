@@ -45,7 +45,6 @@ constexpr int kBlockK = 128;    // columns of a block of x
 constexpr int kScaleK = 64;     // columns of x that share a power of two
 constexpr int kPieces = 3;
 constexpr int kXSlots = 4;      // blocks of x in shared memory
-constexpr unsigned long long kDrainNs = 1000000000ull;
 
 // A block of 128 columns of nt tokens, split: kPieces x [nt][128 bytes], the 16-byte
 // chunks of token t's row at chunk ^ t % 8 (the 128-byte swizzle) and in each 8
@@ -103,16 +102,16 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   return r;
 }
 
-// mbar_wait with everything but the first try out of line.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort,
-                                       unsigned long long limit_ns) {
-  if (mbar_wait(bar, parity, abort, limit_ns)) return true;
-  *abort = 1;
+// A warp waits for phase `parity` of `bar`; false, for all of it, after a limited
+// number of tries (seconds).  The first look is apart from the loop: it nearly
+// always finds the phase over, and a loop costs three times its branch.
+constexpr uint32_t kWaitTries = 1u << 24;
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+#pragma unroll 1
+  for (uint32_t n = kWaitTries; n != 0; --n)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return false;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort,
-                                     unsigned long long limit_ns) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, limit_ns);
 }
 
 // Instruction descriptor: D fp32, A E4M3, B E5M2, both K-major, M = 128.
@@ -221,27 +220,25 @@ struct W4Job {
   const float* wts;
   int P, k;
   int* err;      // status word, or null
-  unsigned long long timeout_ns;
 };
 
 template <int PG, int NT>
 struct W4Shape {
   static constexpr int kN = NT < 16 ? 16 : NT;  // MMA N (16 at least with 128 rows)
   static constexpr int kSumK = PG == 1 ? 32 : kScaleK;  // columns of one accumulator
+  static constexpr int kPerSm = NT == 8 ? 4 : NT == 16 ? 3 : 2;
+  static constexpr int kTmem = NT <= 16 ? 128 : 256;  // columns of tensor memory
   // Columns of a unit, what is multiplied at a time: as many as leave room for
-  // two buffers of A and a unit's accumulators in 128 columns of tensor memory.
-  static constexpr bool fits(int unit) { return unit / 2 + kN * (unit / kSumK) <= 128; }
+  // two buffers of A and two sets of accumulators (one is read during the next
+  // unit's MMAs).
+  static constexpr bool fits(int unit) { return unit / 2 + 2 * kN * (unit / kSumK) <= kTmem; }
   static constexpr int kUnitK = fits(128) ? 128 : 64;
   static_assert(fits(kUnitK), "tensor memory");
   static constexpr int kUnits = kBlockK / kUnitK;  // of a block of columns
   static constexpr int kSub = kUnitK / kSumK;      // accumulators of a unit
   static constexpr int kACols = kUnitK / 4;
-  // two sets of accumulators, so that one is read during the next unit's MMAs,
-  // where that fits too
-  static constexpr int kSums = 2 * kACols + 2 * kN * kSub <= 128 ? 2 : 1;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = NT == 8 ? 2 : 3;
   static constexpr int kXBytes = kPieces * x_piece_bytes(NT);
-  static constexpr int kPerSm = NT == 8 ? 3 : 2;
   static constexpr size_t kSmem =
       1024 + static_cast<size_t>(kStages) * kStageBytes + kXSlots * (kXBytes + x_meta_bytes(NT));
 };
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     valid = __popc(__ballot_sync(0xffffffffu, lane < NT && __ldg(ids + min(lane, NT - 1)) < j.P));
   }
   if (warp == 4) {
-    tmem_alloc(&s_tmem, 128);
+    tmem_alloc(&s_tmem, S::kTmem);
     tmem_relinquish();
   }
   __syncthreads();
@@ -379,8 +376,7 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     const uint64_t db0 = sdesc_kmajor_sw128(smem_addr(x_pieces)) -
                          (NT == 8 ? static_cast<uint64_t>(1024 >> 4) << 32 : 0);
     for (int blk = 0; blk < n_blks; ++blk) {
-      const bool there = ok && wait(&s_x[blk % kXSlots], blk / kXSlots & 1, &s_abort, j.timeout_ns);
-      ok = __all_sync(0xffffffffu, there);
+      ok = ok && warp_wait(&s_x[blk % kXSlots], blk / kXSlots & 1);
 #pragma unroll
       for (int h = 0; h < S::kUnits; ++h) {
         const int u = blk * S::kUnits + h;
@@ -389,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
           tc_fence_after_sync();
           const uint64_t db = db0 + blk % kXSlots * (S::kXBytes / 16);
           const uint32_t a = tmem + (u & 1) * S::kACols;
-          const uint32_t d = t_d + (S::kSums == 2 ? (u & 1) * (S::kN * S::kSub) : 0);
+          const uint32_t d = t_d + (u & 1) * (S::kN * S::kSub);
 #pragma unroll
           for (int n = kPieces - 1; n >= 0; --n)  // small pieces first
 #pragma unroll
@@ -412,12 +408,11 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
       if (blk % 2 == 1 && codes_issued < n_steps) ++codes_issued;
       if (blk >= 2 && x_issued < n_blks) ++x_issued;
     }
-    if (!ok && lane == 0) {  // the copies in flight land before the block leaves
-      volatile int never = 0;
+    if (!ok) {  // the copies in flight land before the block leaves
       for (int i = max(0, codes_issued - kStages); i < codes_issued; ++i)
-        mbar_wait(&s_codes[i % kStages], i / kStages & 1, &never, kDrainNs);
+        warp_wait(&s_codes[i % kStages], i / kStages & 1);
       for (int i = max(0, x_issued - kXSlots); i < x_issued; ++i)
-        mbar_wait(&s_x[i % kXSlots], i / kXSlots & 1, &never, kDrainNs);
+        warp_wait(&s_x[i % kXSlots], i / kXSlots & 1);
     }
   } else {
     // ---------------------------------------------------------- codes and sums
@@ -475,12 +470,10 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     uint32_t z_step[(kGroups + 3) / 4];
     // adds unit u's sums, scaled; h: its place in block of columns blk
     auto flush = [&](int u, int blk, int h) {
-      const bool there =
-          ok && wait(&s_done[u & 1], u >> 1 & 1, &s_abort, j.timeout_ns) &&
-          wait(&s_x[blk % kXSlots], blk / kXSlots & 1, &s_abort, j.timeout_ns);
-      ok = __all_sync(0xffffffffu, there);
+      ok = ok && warp_wait(&s_done[u & 1], u >> 1 & 1) &&
+           warp_wait(&s_x[blk % kXSlots], blk / kXSlots & 1);
       tc_fence_after_sync();
-      const uint32_t at = t_d + lanes + (S::kSums == 2 ? (u & 1) * (S::kN * S::kSub) : 0);
+      const uint32_t at = t_d + lanes + (u & 1) * (S::kN * S::kSub);
       const float* meta = x_meta + blk % kXSlots * (x_meta_bytes(NT) / 4);
 #pragma unroll
       for (int i = 0; i < S::kSub; ++i) {
@@ -536,14 +529,13 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
 #pragma unroll
         for (int n = 0; n < S::kACols; n += 16) tmem_st16(a + n, v + n);
         const int prev_blk = h == 0 ? blk - 1 : blk, prev_h = (h + S::kUnits - 1) % S::kUnits;
-        if (S::kSums == 1 && u > 0) flush(u - 1, prev_blk, prev_h);
         tmem_wait_st();
         tc_fence_before_sync();
         // A is in place, and the unit's codes are read.  (After a wait that gave up
         // nothing but this barrier keeps the warps together.)
         if (ok) named_barrier_arrive(1 + (u & 1), kThreads);
         else named_barrier(1 + (u & 1), kThreads);
-        if (S::kSums == 2 && u > 0) flush(u - 1, prev_blk, prev_h);
+        if (u > 0) flush(u - 1, prev_blk, prev_h);
 #pragma unroll
         for (int i = 0; i < S::kSub; ++i) {
           const int g = (hb * kBlkSums + h * S::kSub + i) * S::kSumK / (32 * PG);
@@ -554,8 +546,7 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     };
     int slot = 0, phase = 0;
     for (int step = 0; step < n_steps; ++step) {
-      const bool there = ok && wait(&s_codes[slot], phase, &s_abort, j.timeout_ns);
-      ok = __all_sync(0xffffffffu, there);
+      ok = ok && warp_wait(&s_codes[slot], phase);
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
         s_step[i] = __uint_as_float(!j.scale_bf16 ? s_raw[i]
@@ -582,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
       }
     }
   }
+  if (!ok) s_abort = 1;
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -592,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
   }
   if (warp == 4) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, S::kTmem);
   }
   // the sums over the cluster's slices of K, in rank order, in the stages' space:
   // red[token][row]
@@ -762,13 +754,18 @@ void set_weight(W4Job& j, const W4View& w) {
 
 int w4_block_rows(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : 32; }
 
+int w4_layer_block_rows(int T, int E, int k) {
+  const long long P = static_cast<long long>(T) * k;
+  return T <= 8 || P <= 4ll * E ? 8 : T <= 16 || P <= 8ll * E ? 16 : 32;
+}
+
 size_t w4_split_bytes(long long blocks, int nt, int K) {
   return static_cast<size_t>(blocks) * ((K + kBlockK - 1) / kBlockK) * x_block_bytes(nt);
 }
 
 cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int T, int K, int N,
-                             const W4View& w, void* out, bool out_fp32, uint8_t* scratch,
-                             unsigned long long timeout_ns, int num_sms, cudaStream_t st) {
+                             const W4View& w, void* out, bool out_fp32, uint8_t* scratch, int num_sms,
+                             cudaStream_t st) {
   const int nt = w4_block_rows(T);
   W4Job j{};
   set_weight(j, w);
@@ -781,7 +778,6 @@ cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int
   j.T = T;
   j.out = out;
   j.out_fp32 = out_fp32 ? 1 : 0;
-  j.timeout_ns = timeout_ns;
   const int n_cols = (K + kBlockK - 1) / kBlockK;
   const cudaError_t e =
       launch_pdl(w4_split_kernel, dim3(static_cast<unsigned>(j.n_blocks * n_cols)), dim3(nt * 16),
@@ -793,7 +789,7 @@ cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int
 
 cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
                             const W4LayerParams& p, int num_sms, cudaStream_t st) {
-  const int nt = w4_block_rows(p.T);
+  const int nt = w4_layer_block_rows(p.T, p.E, p.k);
   const long long P = static_cast<long long>(p.T) * p.k;
   W4Job j{};
   set_weight(j, p.w13);
@@ -814,7 +810,6 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   j.P = static_cast<int>(P);
   j.k = p.k;
   j.err = p.err;
-  j.timeout_ns = p.timeout_ns;
   const int n_cols = (p.H + kBlockK - 1) / kBlockK;
   cudaError_t e = launch_pdl(
       w4_split_kernel, dim3(static_cast<unsigned>(j.n_blocks * n_cols)), dim3(nt * 16), 0, st, p.x,
