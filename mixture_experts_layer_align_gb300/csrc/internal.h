@@ -179,7 +179,7 @@ cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int
                              const W4View& w, void* out, bool out_fp32, uint8_t* scratch, int num_sms,
                              cudaStream_t st);
 // Bytes of `blocks` blocks of nt tokens with K columns, split (16-byte aligned).
-size_t w4_split_bytes(long long blocks, int nt, int K);
+size_t w4_split_bytes(long long blocks, int nt, int K, int group);
 struct W4LayerParams {
   const __nv_bfloat16* x;
   W4View w13, w2;

@@ -761,8 +761,8 @@ W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
   const long long pairs = static_cast<long long>(P);
   const long long blocks =
       std::min(pairs, (pairs + std::min<long long>(E, pairs) * (bm - 1)) / bm);
-  L.xq = take(w4_split_bytes(blocks, bm, H));
-  L.hq = take(w4_split_bytes(blocks, bm, I));
+  L.xq = take(w4_split_bytes(blocks, bm, H, 32));
+  L.hq = take(w4_split_bytes(blocks, bm, I, 32));
   L.y = take(sizeof(float) * P * H);
   L.total = off;
   return L;
@@ -827,7 +827,7 @@ moe_status_t moe_fused_forward_timed(const moe_fused_args* a, void* workspace,
 size_t moe_w4_matvec_scratch_size(int T, int K) {
   if (T < 1 || K < 1 || T >= (1 << 20) || K > (1 << 20)) return 0;
   const int nt = w4_block_rows(T);
-  return w4_split_bytes((T + nt - 1) / nt, nt, K);
+  return w4_split_bytes((T + nt - 1) / nt, nt, K, 32);  // the most of any group
 }
 
 moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tensor* w, void* out,
@@ -865,7 +865,7 @@ size_t moe_w4_workspace_size(int T, int H, int I, int E, int top_k) {
 
 int moe_w4_launch_count(int T, int H, int I, int E, int top_k) {
   if (!w4_sizes_ok(T, H, I, E, top_k) || !w4_sizes_supported(T, H, I, top_k)) return -1;
-  return T == 0 ? 0 : 6;  // router, alignment, split of x, gate/up, down, combine
+  return T == 0 ? 0 : 7;  // router, alignment, split, gate/up, split, down, combine
 }
 
 moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t workspace_bytes,

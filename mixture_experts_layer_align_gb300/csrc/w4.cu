@@ -10,14 +10,14 @@
 // exponents share their spacing): the nibbles of a word, spread over bytes by two
 // masks and a shift, are the A operand of tcgen05.mma kind::f8f6f4.  x becomes three
 // E5M2 pieces whose sum it is, one MMA each into the same accumulator:
-// a power of two brings the largest |x| of 64 columns to 2^14 .. 2^15, where x is
+// a power of two brings the largest |x| of a token to 2^14 .. 2^15, where x is
 // an fp16 value of 8 significant bits; a piece is the top byte of what is left (a
 // sign, 5 exponent and 2 mantissa bits: E5M2, three significant bits), so the third
 // leaves nothing but what lies 2^-31 below the largest.  Products are exact and
 // sums are fp32 (the MMA was checked to keep addends 2^-23 below the sum).
 //
-// x is split once for a call, by a kernel of its own (h by the gate/up product's
-// epilogue), into the image that shared memory needs.  A thread block owns 128
+// x, and h, is split once for a call, by a kernel of its own, into the image that
+// shared memory needs.  A thread block owns 128
 // weight rows and a slice of K; the blocks of a cluster share rows and split K.  TMA
 // brings 256 columns of the codes (128 bytes of a row) a stage, and x block by block
 // of 128 columns.  Four warps, a thread per row, spread the codes of a unit into
@@ -42,20 +42,28 @@ constexpr int kStageBytes = kRows * kStepK / 2;
 constexpr int kRowThreads = 128;  // one per row
 constexpr int kThreads = kRowThreads + 32;
 constexpr int kBlockK = 128;    // columns of a block of x
-constexpr int kScaleK = 64;     // columns of x that share a power of two
 constexpr int kPieces = 3;
+constexpr int kSplitThreads = 512;
 constexpr int kXSlots = 4;      // blocks of x in shared memory
 
-// A block of 128 columns of nt tokens, split: kPieces x [nt][128 bytes], the 16-byte
-// chunks of token t's row at chunk ^ t % 8 (the 128-byte swizzle) and in each 8
-// columns the order of the spread codes, 0 2 4 6 1 3 5 7; then fp32 [6][nt]: 2^-9
-// times the sum of the scaled x by 32 columns (4, or the first 2 by 64), and for each
-// 64 columns the factor that undoes the scaling of x and of the codes.
+// nt tokens, split: for each block of 128 columns kPieces x [nt][128 bytes], the
+// 16-byte chunks of token t's row at chunk ^ t % 8 (the 128-byte swizzle) and in each
+// 8 columns the order of the spread codes, 0 2 4 6 1 3 5 7; then for each block (an
+// even number of them) fp32 [128 / group][nt], 2^-9 times the sums of the scaled x;
+// then fp32 [nt], the factors that undo the scaling of x and of the codes.
 __host__ __device__ constexpr int x_piece_bytes(int nt) { return nt * kBlockK; }
-__host__ __device__ constexpr int x_meta_bytes(int nt) { return 6 * nt * 4; }
-__host__ __device__ constexpr int x_block_bytes(int nt) {
-  return kPieces * x_piece_bytes(nt) + x_meta_bytes(nt);
-}
+struct XLayout {
+  int n_cols, nt, per_block;  // blocks of columns, tokens, sums of a block
+  __host__ __device__ XLayout(int K, int nt_, int group)
+      : n_cols((K + kBlockK - 1) / kBlockK), nt(nt_), per_block(kBlockK / group * nt_) {}
+  __host__ __device__ size_t sums() const {
+    return static_cast<size_t>(n_cols) * kPieces * x_piece_bytes(nt);
+  }
+  __host__ __device__ size_t factors() const {
+    return sums() + static_cast<size_t>(n_cols + n_cols % 2) * per_block * 4;
+  }
+  __host__ __device__ size_t bytes() const { return factors() + nt * 4; }  // a multiple of 16
+};
 
 __device__ __forceinline__ void load_raw(uint32_t* r, const uint2* p) {
   const uint2 v = __ldg(p);
@@ -119,80 +127,96 @@ __device__ constexpr uint32_t w4_idesc(int N) {
   return (1u << 4) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Splits 8 columns (c8 = column / 8 of the block) of token t; every lane of a
-// warp calls it, eight consecutive lanes holding 64 columns of a token.  v: the
-// values, or NaN or infinities among them: their token's factor becomes NaN, and a
-// NaN sum is formed again without the split.
-__device__ __forceinline__ void split8(uint8_t* block, int nt, int t, int c8, const float (&v)[8],
-                                       bool by32) {
-  float m = 0.f;
-  bool finite = true;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m = fmaxf(m, fabsf(v[i]));
-    finite = finite && isfinite(v[i]);
-  }
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const unsigned bad = __ballot_sync(0xffffffffu, !finite);
-  finite = (bad >> (threadIdx.x & 24) & 0xffu) == 0u;
-  // biased exponent of the largest; at least 14, so that the scale stays finite
-  const int ex = max(finite ? static_cast<int>(__float_as_uint(m) >> 23) : 0, 14);
-  const float scale = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(141 - ex)
-  float sum = 0.f;
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = finite ? v[2 * i] * scale : 0.f, hi = finite ? v[2 * i + 1] * scale : 0.f;
-    sum += lo + hi;
-    h[i] = cvt_f16x2(lo, hi);
-  }
-  uint8_t* p = block + t * 128 + ((c8 / 2) ^ (t & 7)) * 16 + c8 % 2 * 8;
-#pragma unroll
-  for (int n = 0; n < kPieces; ++n) {
-    const uint32_t a = __byte_perm(h[0], h[1], 0x7351), b = __byte_perm(h[2], h[3], 0x7351);
-    *reinterpret_cast<uint2*>(p + n * x_piece_bytes(nt)) =
-        make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-#pragma unroll
-    for (int q = 0; q < 4; ++q) h[q] = sub_f16x2(h[q], h[q] & 0xff00ff00u);
-  }
-  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  if (!by32) sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-  float* meta = reinterpret_cast<float*>(block + kPieces * x_piece_bytes(nt));
-  if (by32 ? c8 % 4 == 0 : c8 % 8 == 0) meta[(by32 ? c8 / 4 : c8 / 8) * nt + t] = 0x1p-9f * sum;
-  if (c8 % 8 == 0)
-    meta[(4 + c8 / 8) * nt + t] =
-        finite ? __uint_as_float(static_cast<uint32_t>(ex - 5) << 23) : __int_as_float(0x7fc00000);
-}
-
-// x, split: a thread block for each block of tokens and of 128 columns, 16 threads a
-// token.  Layer: the tokens of the pairs in sorted_ids.
-__global__ void __launch_bounds__(512)
-    w4_split_kernel(const __nv_bfloat16* __restrict__ x, int T, int K, int nt, int by32,
+// x, split: a thread block for each token.  Layer: the rows of the pairs in
+// sorted_ids, row pair / k of x.  A token with infinities or NaN gets the factor NaN:
+// its sums, not numbers then, are formed again from x itself.
+__global__ void __launch_bounds__(kSplitThreads)
+    w4_split_kernel(const __nv_bfloat16* __restrict__ x, int T, int K, int nt, int group,
                     uint8_t* __restrict__ xq, const int32_t* __restrict__ sorted_ids,
                     const int32_t* __restrict__ num_padded, int P, int k) {
+  __shared__ float s_max[kSplitThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int n_cols = (K + kBlockK - 1) / kBlockK;
-  const int block = blockIdx.x / n_cols, blk = blockIdx.x % n_cols;
-  if (sorted_ids != nullptr && block * nt >= __ldg(num_padded)) return;
-  const int t = threadIdx.x / 16, c8 = threadIdx.x % 16, col = blk * kBlockK + c8 * 8;
-  long long row = static_cast<long long>(block) * nt + t;
-  bool on;
+  const int block = blockIdx.x / nt, t = blockIdx.x % nt;
+  long long row = blockIdx.x;
   if (sorted_ids != nullptr) {
+    if (row >= __ldg(num_padded)) return;
     const int pair = __ldg(sorted_ids + row);
-    on = pair < P;
+    if (pair >= P) return;
     row = pair / k;
-  } else {
-    on = row < T;
+  } else if (row >= T) {
+    return;
   }
-  float v[8];
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (on && col < K) w = __ldg(reinterpret_cast<const uint4*>(x + row * K + col));
-  v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-  v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
-  split8(xq + (static_cast<size_t>(block) * n_cols + blk) * x_block_bytes(nt), nt, t, c8, v, by32);
+  const XLayout lay(K, nt, group);
+  const uint4* src = reinterpret_cast<const uint4*>(x + row * K);
+  uint8_t* to = xq + block * lay.bytes();
+  const int tid = threadIdx.x, n8 = K / 8;
+  constexpr int kKeep = 4;  // loads kept from the first pass
+  uint4 keep[kKeep];
+  uint32_t m = 0;
+  auto top = [&](const uint4& w) {
+    m = max_bf16x2(m, max_bf16x2(max_bf16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                 max_bf16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    keep[i] = tid + i * kSplitThreads < n8 ? __ldg(src + tid + i * kSplitThreads) : make_uint4(0, 0, 0, 0);
+    top(keep[i]);
+  }
+  for (int i = tid + kKeep * kSplitThreads; i < n8; i += kSplitThreads) top(__ldg(src + i));
+  m = max_bf16x2(m, m >> 16 | m << 16);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // (magnitudes as integers order like the numbers, NaN above all)
+  if (tid % 32 == 0) s_max[tid / 32] = __uint_as_float(m << 16);
+  __syncthreads();
+  uint32_t top_bits = 0;
+#pragma unroll
+  for (int i = 0; i < kSplitThreads / 32; ++i) top_bits = max(top_bits, __float_as_uint(s_max[i]));
+  const bool finite = top_bits < 0x7f800000u;
+  // biased exponent of the largest; at least 14, so that the scale stays finite
+  const int ex = max(finite ? static_cast<int>(top_bits >> 23) : 0, 14);
+  const float scale = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(141 - ex)
+  const uint64_t scale2 = pack2(scale, scale);
+  if (tid == 0)
+    reinterpret_cast<float*>(to + lay.factors())[t] =
+        finite ? __uint_as_float(static_cast<uint32_t>(ex - 5) << 23) : __int_as_float(0x7fc00000);
+  float* sums = reinterpret_cast<float*>(to + lay.sums());
+  const int n8_pad = lay.n_cols * (kBlockK / 8);
+#pragma unroll 1
+  for (int i = tid; i < n8_pad; i += kSplitThreads) {  // whole half warps: a block is 16 threads
+    uint4 w = i < n8 && finite ? (i < kSplitThreads       ? keep[0]
+                                  : i < 2 * kSplitThreads ? keep[1]
+                                  : i < 3 * kSplitThreads ? keep[2]
+                                  : i < 4 * kSplitThreads ? keep[3]
+                                                   : __ldg(src + i))
+                               : make_uint4(0, 0, 0, 0);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    float sum = 0.f;
+    uint32_t h[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      float lo, hi;
+      unpack2(mul2(pack2(bf16_lo(ww[n]), bf16_hi(ww[n])), scale2), lo, hi);
+      sum += lo + hi;
+      h[n] = cvt_f16x2(lo, hi);
+    }
+    const int blk = i / 16, c8 = i % 16;
+    uint8_t* p = to + static_cast<size_t>(blk) * kPieces * x_piece_bytes(nt) + t * 128 +
+                 ((c8 / 2) ^ (t & 7)) * 16 + c8 % 2 * 8;
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+      const uint32_t a = __byte_perm(h[0], h[1], 0x7351), b = __byte_perm(h[2], h[3], 0x7351);
+      *reinterpret_cast<uint2*>(p + n * x_piece_bytes(nt)) =
+          make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) h[q] = sub_f16x2(h[q], h[q] & 0xff00ff00u);
+    }
+    const unsigned half = 0xffffu << (tid & 16);
+    for (int o = 1; o < group / 8; o <<= 1) sum += __shfl_xor_sync(half, sum, o);
+    if (c8 % (group / 8) == 0)
+      sums[static_cast<size_t>(blk) * lay.per_block + c8 / (group / 8) * nt + t] = 0x1p-9f * sum;
+  }
 }
 
 enum W4Mode { kMatvec, kGateUp, kDown };
@@ -205,13 +229,11 @@ struct W4Job {
   int mode, K;
   int n_rows;    // rows of the result: N, I or H
   int n_blocks;  // blocks of tokens (an upper bound for the layer)
-  const uint8_t* xq;        // x (down: h), split: [token block][column block]
+  const uint8_t* xq;        // x (down: h), split: an XLayout for each block of tokens
   const __nv_bfloat16* x;   // tokens (down: h by pair)
   int T;
   void* out;     // matvec: [T][N]; gate/up: h bf16 [pair][I]; down: y fp32 [pair][H]
   int out_fp32;
-  uint8_t* hq;   // gate/up: h, split
-  int h_by32;    // w2's groups are of 32 columns
   int cluster;   // thread blocks that split K
   // layer
   const int32_t* sorted_ids;
@@ -225,22 +247,23 @@ struct W4Job {
 template <int PG, int NT>
 struct W4Shape {
   static constexpr int kN = NT < 16 ? 16 : NT;  // MMA N (16 at least with 128 rows)
-  static constexpr int kSumK = PG == 1 ? 32 : kScaleK;  // columns of one accumulator
   static constexpr int kPerSm = NT == 8 ? 4 : NT == 16 ? 3 : 2;
   static constexpr int kTmem = NT <= 16 ? 128 : 256;  // columns of tensor memory
   // Columns of a unit, what is multiplied at a time: as many as leave room for
   // two buffers of A and two sets of accumulators (one is read during the next
   // unit's MMAs).
-  static constexpr bool fits(int unit) { return unit / 2 + 2 * kN * (unit / kSumK) <= kTmem; }
+  static constexpr bool fits(int unit) { return unit / 2 + 2 * kN * (unit / (32 * PG)) <= kTmem; }
   static constexpr int kUnitK = fits(128) ? 128 : 64;
-  static_assert(fits(kUnitK), "tensor memory");
+  static_assert(fits(kUnitK) && kUnitK >= 32 * PG, "a unit holds whole groups");
   static constexpr int kUnits = kBlockK / kUnitK;  // of a block of columns
-  static constexpr int kSub = kUnitK / kSumK;      // accumulators of a unit
+  static constexpr int kSub = kUnitK / (32 * PG);  // groups, so accumulators, of a unit
   static constexpr int kACols = kUnitK / 4;
   static constexpr int kStages = NT == 8 ? 2 : 3;
   static constexpr int kXBytes = kPieces * x_piece_bytes(NT);
-  static constexpr size_t kSmem =
-      1024 + static_cast<size_t>(kStages) * kStageBytes + kXSlots * (kXBytes + x_meta_bytes(NT));
+  static constexpr int kSumSlots = kStages + 1;              // stages' sums of x
+  static constexpr int kSumBytes = 2 * (4 / PG) * NT * 4;    // of the two blocks of a stage
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes +
+                                  kXSlots * kXBytes + kSumSlots * kSumBytes;
 };
 
 // sum_k x[k] (code[k] - zero) * scale over columns k0 .. k1 of a weight row,
@@ -272,14 +295,14 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
   using S = W4Shape<PG, NT>;
   constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_codes[kStages];  // a stage's codes are there
+  __shared__ uint64_t s_codes[kStages];  // a stage's codes and sums of x are there
   __shared__ uint64_t s_x[kXSlots];      // a block of x is there
   __shared__ uint64_t s_done[2];         // even and odd units' MMAs are done
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   uint8_t* x_pieces = smem + kStages * kStageBytes;
-  float* x_meta = reinterpret_cast<float*>(x_pieces + kXSlots * S::kXBytes);
+  float* x_sums = reinterpret_cast<float*>(x_pieces + kXSlots * S::kXBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int CS = j.cluster;
   const int rank = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -292,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     s_abort = 0;
     fence_mbarrier_init();
   }
-  pdl_wait();
-  pdl_trigger();
+  // Up to pdl_wait() nothing is read that the kernel before, which splits x, writes:
+  // the weights and the lists of the alignment are older than it.
 
   // which rows and tokens; a block past the layer's last one leaves (all of its
   // cluster does)
@@ -338,36 +361,43 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
 
   if (warp == 4) {
     // ---------------------------------------------------------- copies and MMAs
+    const XLayout lay(j.K, NT, 32 * PG);
+    const uint8_t* xq = j.xq + block * lay.bytes();
     auto issue_codes = [&](int step) {
       uint64_t* bar = &s_codes[step % kStages];
       uint8_t* dst = smem + step % kStages * kStageBytes;
-      mbar_arrive_expect_tx(bar, kStageBytes);
+      mbar_arrive_expect_tx(bar, kStageBytes + S::kSumBytes);
       const int col = (step0 + step) * (kStepK / 2), row_a = static_cast<int>(expert_row) + r0;
       tma_load_2d(dst, &map, bar, col, row_a);
       tma_load_2d(dst + kStageBytes / 2, &map, bar, col,
                   row_a + (j.mode == kGateUp ? j.n_rows : kRows / 2));
     };
+    auto issue_sums = [&](int step) {
+      bulk_load(x_sums + step % S::kSumSlots * (S::kSumBytes / 4),
+                xq + lay.sums() + static_cast<size_t>(step0 + step) * S::kSumBytes, S::kSumBytes,
+                &s_codes[step % kStages]);
+    };
     const int x_rows = (valid + 7) / 8 * 8;
-    const uint8_t* xq =
-        j.xq + (static_cast<size_t>(block) * ((j.K + kBlockK - 1) / kBlockK) + k0 / kBlockK) *
-                   x_block_bytes(NT);
     auto issue_x = [&](int blk) {
-      const int slot = blk % kXSlots;
-      uint64_t* bar = &s_x[slot];
-      uint8_t* dst = x_pieces + slot * S::kXBytes;
-      const uint8_t* src = xq + static_cast<size_t>(blk) * x_block_bytes(NT);
-      mbar_arrive_expect_tx(bar, kPieces * x_rows * 128 + x_meta_bytes(NT));
+      uint64_t* bar = &s_x[blk % kXSlots];
+      uint8_t* dst = x_pieces + blk % kXSlots * S::kXBytes;
+      const uint8_t* src = xq + static_cast<size_t>(k0 / kBlockK + blk) * S::kXBytes;
+      mbar_arrive_expect_tx(bar, kPieces * x_rows * 128);
       if (x_rows == NT) {
         bulk_load(dst, src, S::kXBytes, bar);
       } else {
         for (int n = 0; n < kPieces; ++n)
           bulk_load(dst + n * x_piece_bytes(NT), src + n * x_piece_bytes(NT), x_rows * 128, bar);
       }
-      bulk_load(x_meta + slot * (x_meta_bytes(NT) / 4), src + S::kXBytes, x_meta_bytes(NT), bar);
     };
     int codes_issued = min(kStages, n_steps), x_issued = min(kXSlots, n_blks);
-    if (elect_one()) {
+    if (elect_one())
       for (int i = 0; i < codes_issued; ++i) issue_codes(i);
+    __syncwarp();
+    pdl_wait();
+    pdl_trigger();
+    if (elect_one()) {
+      for (int i = 0; i < codes_issued; ++i) issue_sums(i);
       for (int i = 0; i < x_issued; ++i) issue_x(i);
     }
     __syncwarp();
@@ -390,9 +420,9 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
           for (int n = kPieces - 1; n >= 0; --n)  // small pieces first
 #pragma unroll
             for (int i = 0; i < S::kUnitK / 32; ++i)
-              umma_f8_ts(d + i / (S::kSumK / 32) * S::kN, a + i * 8,
+              umma_f8_ts(d + i / PG * S::kN, a + i * 8,
                          db + n * (x_piece_bytes(NT) / 16) + (h * (S::kUnitK / 32) + i) * 2, idesc,
-                         n < kPieces - 1 || i % (S::kSumK / 32) != 0);
+                         n < kPieces - 1 || i % PG != 0);
           umma_commit(&s_done[u & 1]);
         }
         __syncwarp();
@@ -401,7 +431,10 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
       // before the last: a stage is free after its second block, and x's buffer of
       // two blocks ago too.
       if (ok && elect_one()) {
-        if (blk % 2 == 1 && codes_issued < n_steps) issue_codes(codes_issued);
+        if (blk % 2 == 1 && codes_issued < n_steps) {
+          issue_codes(codes_issued);
+          issue_sums(codes_issued);
+        }
         if (blk >= 2 && x_issued < n_blks) issue_x(x_issued);
       }
       __syncwarp();
@@ -419,6 +452,17 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const int groups = (j.K + 32 * PG - 1) / (32 * PG);
     const size_t group0 = grow * groups + k0 / (32 * PG);
+    // the row's scales and zero points of this slice on their way to L2
+    {
+      const int n = (k1 - k0 + 32 * PG - 1) / (32 * PG), lg = j.scale_bf16 ? 1 : 2;
+      const uint8_t* p = static_cast<const uint8_t*>(j.scales) + (group0 << lg);
+      for (int i = 0; i < n << lg; i += 128) prefetch_l2(p + i);
+      prefetch_l2(p + ((n - 1) << lg));
+      if (ZP) {
+        for (int i = 0; i < n; i += 128) prefetch_l2(j.zeros + group0 + i);
+        prefetch_l2(j.zeros + group0 + n - 1);
+      }
+    }
     // Scales and zero points of a stage's groups, as they lie in memory: one load
     // each when every row's stage starts on its size (K a multiple of the stage's
     // columns), else group by group.
@@ -464,49 +508,50 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
 #pragma unroll
     for (int i = 0; i < (kGroups + 3) / 4; ++i) z_raw[i] = 0;
     fetch_scales(0);
-    // scales of the blocks of a stage by accumulator
-    constexpr int kBlkSums = kBlockK / S::kSumK;
+    constexpr int kBlkGroups = 4 / PG;
     float s_step[kGroups], s_old[S::kSub], z_old[S::kSub];
     uint32_t z_step[(kGroups + 3) / 4];
-    // adds unit u's sums, scaled; h: its place in block of columns blk
-    auto flush = [&](int u, int blk, int h) {
-      ok = ok && warp_wait(&s_done[u & 1], u >> 1 & 1) &&
-           warp_wait(&s_x[blk % kXSlots], blk / kXSlots & 1);
+    const float* sums_old = x_sums;  // of the last unit's groups
+    // adds unit u's sums, scaled
+    auto flush = [&](int u) {
+      float4 xs[NT <= 8 ? S::kSub : 1][2];
+      if (NT <= 8) {
+#pragma unroll
+        for (int i = 0; i < S::kSub; ++i) {
+          xs[i][0] = *reinterpret_cast<const float4*>(sums_old + i * NT);
+          xs[i][1] = *reinterpret_cast<const float4*>(sums_old + i * NT + 4);
+        }
+      }
+      ok = ok && warp_wait(&s_done[u & 1], u >> 1 & 1);
       tc_fence_after_sync();
       const uint32_t at = t_d + lanes + (u & 1) * (S::kN * S::kSub);
-      const float* meta = x_meta + blk % kXSlots * (x_meta_bytes(NT) / 4);
 #pragma unroll
-      for (int i = 0; i < S::kSub; ++i) {
-        const uint64_t zz = pack2(-z_old[i], -z_old[i]), ss = pack2(s_old[i], s_old[i]);
-        const float* sum = meta + (h * S::kSub + i) * NT;
-        const float* factor = meta + (4 + (h * S::kSub + i) * S::kSumK / kScaleK) * NT;
+      for (int t0 = 0; t0 < NT; t0 += 8) {
+        if (t0 > 0 && t0 >= valid) break;
+        uint32_t d[S::kSub][8];
 #pragma unroll
-        for (int t0 = 0; t0 < NT; t0 += 8) {
-          if (t0 > 0 && t0 >= valid) break;
-          uint32_t d[8];
-          tmem_ld8_async(at + i * S::kN + t0, d);
-          float4 xs[2], f[2];
+        for (int i = 0; i < S::kSub; ++i) tmem_ld8_async(at + i * S::kN + t0, d[i]);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            xs[n] = *reinterpret_cast<const float4*>(sum + t0 + 4 * n);
-            f[n] = *reinterpret_cast<const float4*>(factor + t0 + 4 * n);
-          }
-          tmem_wait_ld8(d);
+        for (int i = 0; i < S::kSub; ++i) {
+          tmem_wait_ld8(d[i]);
+          const uint64_t zz = pack2(-z_old[i], -z_old[i]), ss = pack2(s_old[i], s_old[i]);
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            const float4 xv = xs[n / 2], fv = f[n / 2];
+            const float4 xv = NT <= 8 ? xs[i][n / 2]
+                                      : *reinterpret_cast<const float4*>(sums_old + i * NT + t0 +
+                                                                         n / 2 * 4);
             const uint64_t x2 = n % 2 ? pack2(xv.z, xv.w) : pack2(xv.x, xv.y);
-            const uint64_t f2 = n % 2 ? pack2(fv.z, fv.w) : pack2(fv.x, fv.y);
-            const uint64_t d2 = pack2(__uint_as_float(d[2 * n]), __uint_as_float(d[2 * n + 1]));
+            const uint64_t d2 =
+                pack2(__uint_as_float(d[i][2 * n]), __uint_as_float(d[i][2 * n + 1]));
             float& lo = acc[t0 + 2 * n];
             float& hi = acc[t0 + 2 * n + 1];
-            unpack2(fma2(ss, mul2(f2, fma2(zz, x2, d2)), pack2(lo, hi)), lo, hi);
+            unpack2(fma2(ss, fma2(zz, x2, d2), pack2(lo, hi)), lo, hi);
           }
         }
       }
     };
     // a block of 128 columns, the hb-th of its stage
-    auto columns = [&](int blk, int slot, auto which) {
+    auto columns = [&](int blk, int slot, const float* sums, auto which) {
       constexpr int hb = decltype(which)::value;
       const uint8_t* codes = smem + slot * kStageBytes + tid * 128;
 #pragma unroll
@@ -528,25 +573,24 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
         const uint32_t a = tmem + (u & 1) * S::kACols + lanes;
 #pragma unroll
         for (int n = 0; n < S::kACols; n += 16) tmem_st16(a + n, v + n);
-        const int prev_blk = h == 0 ? blk - 1 : blk, prev_h = (h + S::kUnits - 1) % S::kUnits;
         tmem_wait_st();
         tc_fence_before_sync();
         // A is in place, and the unit's codes are read.  (After a wait that gave up
         // nothing but this barrier keeps the warps together.)
         if (ok) named_barrier_arrive(1 + (u & 1), kThreads);
         else named_barrier(1 + (u & 1), kThreads);
-        if (u > 0) flush(u - 1, prev_blk, prev_h);
+        if (u > 0) flush(u - 1);
 #pragma unroll
         for (int i = 0; i < S::kSub; ++i) {
-          const int g = (hb * kBlkSums + h * S::kSub + i) * S::kSumK / (32 * PG);
+          const int g = hb * kBlkGroups + h * S::kSub + i;
           s_old[i] = s_step[g];
           z_old[i] = ZP ? static_cast<float>(z_step[g / 4] >> (8 * (g % 4)) & 0xffu) : 8.f;
         }
+        sums_old = sums + (hb * kBlkGroups + h * S::kSub) * NT;
       }
     };
-    int slot = 0, phase = 0;
+    int slot = 0, phase = 0, sum_slot = 0;
     for (int step = 0; step < n_steps; ++step) {
-      ok = ok && warp_wait(&s_codes[slot], phase);
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
         s_step[i] = __uint_as_float(!j.scale_bf16 ? s_raw[i]
@@ -555,11 +599,23 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
 #pragma unroll
       for (int i = 0; i < (kGroups + 3) / 4; ++i) z_step[i] = z_raw[i];
       fetch_scales(step + 1);
-      columns(2 * step, slot, std::integral_constant<int, 0>{});
-      if (2 * step + 1 < n_blks) columns(2 * step + 1, slot, std::integral_constant<int, 1>{});
+      ok = ok && warp_wait(&s_codes[slot], phase);
+      const float* sums = x_sums + sum_slot * (S::kSumBytes / 4);
+      columns(2 * step, slot, sums, std::integral_constant<int, 0>{});
+      if (2 * step + 1 < n_blks)
+        columns(2 * step + 1, slot, sums, std::integral_constant<int, 1>{});
       if (++slot == kStages) slot = 0, phase ^= 1;
+      if (++sum_slot == S::kSumSlots) sum_slot = 0;
     }
-    flush(n_blks * S::kUnits - 1, n_blks - 1, S::kUnits - 1);
+    flush(n_blks * S::kUnits - 1);
+    pdl_wait();  // (what follows reads what the kernel before wrote, without a barrier)
+    {
+      const XLayout lay(j.K, NT, 32 * PG);
+      const float* factors = reinterpret_cast<const float*>(j.xq + block * lay.bytes() + lay.factors());
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t < valid) acc[t] *= __ldg(factors + t);
+    }
     // a sum that is not a number: as the weights and tokens have it, column by column
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -604,54 +660,23 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
       v += ld_cluster_f32(mapa_shared(red_at + (t * kRows + r) * 4, i));
     return v;
   };
-  if (j.mode == kGateUp) {
-    // h of this rank's tokens (rank, rank + CS, ..), kept in bf16 and split
-    float* hs = red + NT * kRows;  // [token][64]
-    const int mine = rank < valid ? (valid - rank + CS - 1) / CS : 0;
-    for (int i = tid; i < mine * rows_out; i += kThreads) {
-      const int t = rank + i / rows_out * CS, r = i % rows_out;
-      float h = 0.f;
-      if (r0 + r < j.n_rows) {
-        const float gate = sum(t, r), up = sum(t, r + rows_out);
-        const __nv_bfloat16 b = __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
-        const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
-        static_cast<__nv_bfloat16*>(j.out)[static_cast<size_t>(pair) * j.n_rows + r0 + r] = b;
-        h = __bfloat162float(b);
-      }
-      hs[i] = h;
-    }
-    __syncthreads();
-    const int n_cols = (j.n_rows + kBlockK - 1) / kBlockK;
-    uint8_t* to = j.hq + (static_cast<size_t>(block) * n_cols + r0 / kBlockK) * x_block_bytes(NT);
-    // eight threads a token; the last rows of h also stand for the block's other
-    // half, zeros, where no thread block has it
-    const bool both = r0 % kBlockK == 0 && r0 + rows_out >= j.n_rows;
-    for (int i0 = 0; i0 < mine * 8; i0 += kThreads) {
-      const int i = i0 + tid, ti = min(i / 8, max(mine - 1, 0)), c = i % 8;
-      const int t = rank + ti * CS;
-      float v[8];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) v[n] = hs[ti * rows_out + c * 8 + n];
-      split8(to, NT, t, r0 % kBlockK / 8 + c, v, j.h_by32);
-      if (both) {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) v[n] = 0.f;
-        split8(to, NT, t, 8 + c, v, j.h_by32);
-      }
-    }
-  } else {
-    for (int i = rank * kThreads + tid; i < rows_out * valid; i += CS * kThreads) {
-      const int t = i / rows_out, r = i % rows_out;
-      if (r0 + r >= j.n_rows) continue;
+  for (int i = rank * kThreads + tid; i < rows_out * valid; i += CS * kThreads) {
+    const int t = i / rows_out, r = i % rows_out;
+    if (r0 + r >= j.n_rows) continue;
+    if (j.mode == kMatvec) {
       const float v = sum(t, r);
-      if (j.mode == kMatvec) {
-        const size_t o = (static_cast<size_t>(block) * NT + t) * j.n_rows + r0 + r;
-        if (j.out_fp32) static_cast<float*>(j.out)[o] = v;
-        else static_cast<__nv_bfloat16*>(j.out)[o] = __float2bfloat16_rn(v);
+      const size_t o = (static_cast<size_t>(block) * NT + t) * j.n_rows + r0 + r;
+      if (j.out_fp32) static_cast<float*>(j.out)[o] = v;
+      else static_cast<__nv_bfloat16*>(j.out)[o] = __float2bfloat16_rn(v);
+    } else {
+      const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
+      const size_t o = static_cast<size_t>(pair) * j.n_rows + r0 + r;
+      if (j.mode == kGateUp) {
+        const float gate = sum(t, r), up = sum(t, r + rows_out);
+        static_cast<__nv_bfloat16*>(j.out)[o] =
+            __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
       } else {
-        const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
-        static_cast<float*>(j.out)[static_cast<size_t>(pair) * j.n_rows + r0 + r] =
-            __ldg(j.wts + pair) * v;
+        static_cast<float*>(j.out)[o] = __ldg(j.wts + pair) * sum(t, r);
       }
     }
   }
@@ -759,13 +784,25 @@ int w4_layer_block_rows(int T, int E, int k) {
   return T <= 8 || P <= 4ll * E ? 8 : T <= 16 || P <= 8ll * E ? 16 : 32;
 }
 
-size_t w4_split_bytes(long long blocks, int nt, int K) {
-  return static_cast<size_t>(blocks) * ((K + kBlockK - 1) / kBlockK) * x_block_bytes(nt);
+size_t w4_split_bytes(long long blocks, int nt, int K, int group) {
+  return static_cast<size_t>(blocks) * XLayout(K, nt, group).bytes();
 }
 
+namespace {
+
+cudaError_t launch_split(const __nv_bfloat16* x, int T, int K, int n_blocks, int nt, int group,
+                         uint8_t* xq, const int32_t* sorted_ids, const int32_t* num_padded, int P,
+                         int k, cudaStream_t st) {
+  return launch_pdl(w4_split_kernel, dim3(static_cast<unsigned>(n_blocks) * nt), dim3(kSplitThreads),
+                    0, st,
+                    x, T, K, nt, group, xq, sorted_ids, num_padded, P, k);
+}
+
+}  // namespace
+
 cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int T, int K, int N,
-                             const W4View& w, void* out, bool out_fp32, uint8_t* scratch, int num_sms,
-                             cudaStream_t st) {
+                             const W4View& w, void* out, bool out_fp32, uint8_t* scratch,
+                             int num_sms, cudaStream_t st) {
   const int nt = w4_block_rows(T);
   W4Job j{};
   set_weight(j, w);
@@ -778,11 +815,8 @@ cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int
   j.T = T;
   j.out = out;
   j.out_fp32 = out_fp32 ? 1 : 0;
-  const int n_cols = (K + kBlockK - 1) / kBlockK;
   const cudaError_t e =
-      launch_pdl(w4_split_kernel, dim3(static_cast<unsigned>(j.n_blocks * n_cols)), dim3(nt * 16),
-                 0, st, x, T, K, nt, w.group == 32 ? 1 : 0, scratch,
-                 static_cast<const int32_t*>(nullptr), static_cast<const int32_t*>(nullptr), 0, 1);
+      launch_split(x, T, K, j.n_blocks, nt, w.group, scratch, nullptr, nullptr, 0, 1, st);
   if (e != cudaSuccess) return e;
   return launch_job(map, w.group, j, nt, num_sms, st);
 }
@@ -801,8 +835,6 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   j.x = p.x;
   j.T = p.T;
   j.out = p.h;
-  j.hq = p.hq;
-  j.h_by32 = p.w2.group == 32 ? 1 : 0;
   j.sorted_ids = p.sorted_ids;
   j.block_expert = p.block_expert;
   j.num_padded = p.num_padded;
@@ -810,13 +842,12 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   j.P = static_cast<int>(P);
   j.k = p.k;
   j.err = p.err;
-  const int n_cols = (p.H + kBlockK - 1) / kBlockK;
-  cudaError_t e = launch_pdl(
-      w4_split_kernel, dim3(static_cast<unsigned>(j.n_blocks * n_cols)), dim3(nt * 16), 0, st, p.x,
-      p.T, p.H, nt, p.w13.group == 32 ? 1 : 0, p.xq, p.sorted_ids, p.num_padded,
-      static_cast<int>(P), p.k);
-  if (e != cudaSuccess) return e;
-  e = launch_job(map13, p.w13.group, j, nt, num_sms, st);
+  cudaError_t e = launch_split(p.x, p.T, p.H, j.n_blocks, nt, p.w13.group, p.xq, p.sorted_ids,
+                               p.num_padded, j.P, p.k, st);
+  if (e == cudaSuccess) e = launch_job(map13, p.w13.group, j, nt, num_sms, st);
+  if (e == cudaSuccess)
+    e = launch_split(p.h, 0, p.I, j.n_blocks, nt, p.w2.group, p.hq, p.sorted_ids, p.num_padded,
+                     j.P, 1, st);
   if (e != cudaSuccess) return e;
   set_weight(j, p.w2);
   j.mode = kDown;
