@@ -499,15 +499,17 @@ def moe_w4_matvec(x, w: W4Tensor, out=None, out_dtype=None, scratch=None, stream
     if out.dtype not in (torch.bfloat16, torch.float32) or out_dtype not in (None, out.dtype):
         raise ValueError(f"out must be bfloat16 or float32 (out_dtype {out_dtype}), got {out.dtype}")
     _require(out, out.dtype, "out", (T, N))
+    L = load()
     if scratch is None:
-        scratch = torch.empty(max(16, moe_w4_matvec_scratch_size(T, K)), dtype=torch.uint8,
+        scratch = torch.empty(max(16, L.moe_w4_matvec_scratch_size(T, K)), dtype=torch.uint8,
                               device=x.device)
         if stream is not None:
             scratch.record_stream(stream)
-    _require(scratch, torch.uint8, "scratch")
-    _check(load().moe_w4_matvec(_ptr(x), T, K, N, ctypes.byref(w._c), _ptr(out),
-                                MOE_DT_FP32 if out.dtype == torch.float32 else MOE_DT_BF16,
-                                _ptr(scratch), scratch.numel(), _stream(stream)), "moe_w4_matvec")
+    else:
+        _require(scratch, torch.uint8, "scratch")
+    _check(L.moe_w4_matvec(_ptr(x), T, K, N, ctypes.byref(w._c), _ptr(out),
+                           MOE_DT_FP32 if out.dtype == torch.float32 else MOE_DT_BF16,
+                           _ptr(scratch), scratch.numel(), _stream(stream)), "moe_w4_matvec")
     return out
 
 

@@ -28,6 +28,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -38,31 +39,36 @@ namespace {
 
 constexpr int kRows = 128;      // weight rows of a thread block (64 gate and 64 up rows)
 constexpr int kStepK = 256;     // columns of a stage
-constexpr int kStageBytes = kRows * kStepK / 2;
+constexpr int kCodeBytes = kRows * kStepK / 2;  // of a stage
+constexpr int kMaxStages = 6;
+constexpr int kRedTokens = 8, kRedBytes = kRedTokens * kRows * 4;  // sums on their way out
+constexpr int kMaxCluster = 8;
+constexpr int kSmSmem = 228 * 1024, kMaxSmem = 226 * 1024;  // of an SM; dynamic, of a block
+constexpr int kStaticSmem = 1024 + 256;  // what else a block takes of them
 constexpr int kRowThreads = 128;  // one per row
-constexpr int kThreads = kRowThreads + 32;
+constexpr int kThreads = kRowThreads + 64;  // a warp for MMAs, a warp for copies
 constexpr int kBlockK = 128;    // columns of a block of x
 constexpr int kPieces = 3;
-constexpr int kSplitThreads = 512;
-constexpr int kXSlots = 4;      // blocks of x in shared memory
+constexpr int kSplitThreads = 256;
 
-// nt tokens, split: for each block of 128 columns kPieces x [nt][128 bytes], the
+// nt tokens of x, split.  For each block of 128 columns kPieces x [nt][128 bytes], the
 // 16-byte chunks of token t's row at chunk ^ t % 8 (the 128-byte swizzle) and in each
-// 8 columns the order of the spread codes, 0 2 4 6 1 3 5 7; then for each block (an
-// even number of them) fp32 [128 / group][nt], 2^-9 times the sums of the scaled x;
-// then fp32 [nt], the factors that undo the scaling of x and of the codes.
+// 8 columns the order of the spread codes, 0 2 4 6 1 3 5 7; and fp32 [128 / group + 1][nt]:
+// 2^-9 times the sums of the scaled x of its groups, then the factors that undo the
+// scaling of x and of the codes.
 __host__ __device__ constexpr int x_piece_bytes(int nt) { return nt * kBlockK; }
+__host__ __device__ constexpr int x_side_bytes(int nt, int group) {
+  return (kBlockK / group + 1) * nt * 4;
+}
+// Where they lie for all of K: the pieces of every block, then the rest of every block.
 struct XLayout {
-  int n_cols, nt, per_block;  // blocks of columns, tokens, sums of a block
+  int n_cols, nt, side;
   __host__ __device__ XLayout(int K, int nt_, int group)
-      : n_cols((K + kBlockK - 1) / kBlockK), nt(nt_), per_block(kBlockK / group * nt_) {}
-  __host__ __device__ size_t sums() const {
+      : n_cols((K + kStepK - 1) / kStepK * 2), nt(nt_), side(x_side_bytes(nt_, group)) {}
+  __host__ __device__ size_t sides() const {
     return static_cast<size_t>(n_cols) * kPieces * x_piece_bytes(nt);
   }
-  __host__ __device__ size_t factors() const {
-    return sums() + static_cast<size_t>(n_cols + n_cols % 2) * per_block * 4;
-  }
-  __host__ __device__ size_t bytes() const { return factors() + nt * 4; }  // a multiple of 16
+  __host__ __device__ size_t bytes() const { return sides() + static_cast<size_t>(n_cols) * side; }
 };
 
 __device__ __forceinline__ void load_raw(uint32_t* r, const uint2* p) {
@@ -85,6 +91,11 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
@@ -127,96 +138,83 @@ __device__ constexpr uint32_t w4_idesc(int N) {
   return (1u << 4) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// x, split: a thread block for each token.  Layer: the rows of the pairs in
-// sorted_ids, row pair / k of x.  A token with infinities or NaN gets the factor NaN:
-// its sums, not numbers then, are formed again from x itself.
+// 256 columns of a token, split by a warp: w holds the lane's eight.  The pieces of
+// the eight columns go to `to` + n * piece_bytes; `sum` is that of the lane's group,
+// in every lane of it.  Columns with an infinity or NaN get the factor NaN: the sums
+// that they enter are formed again from x itself.
+__device__ __forceinline__ void split_columns(uint4 w, int group_lanes, uint8_t* to,
+                                              int piece_bytes, float& sum, float& factor) {
+  uint32_t m = max_bf16x2(max_bf16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                          max_bf16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  // (magnitudes as integers order like the numbers, infinity and NaN above all)
+  const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) << 16;
+  const bool finite = top < 0x7f800000u;
+  // biased exponent of the largest; at least 14, so that the scale stays finite
+  const int ex = max(finite ? static_cast<int>(top >> 23) : 0, 14);
+  const float scale = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(141 - ex)
+  factor = finite ? __uint_as_float(static_cast<uint32_t>(ex - 5) << 23) : __int_as_float(0x7fc00000);
+  const uint64_t scale2 = pack2(scale, scale);
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+  uint64_t s2 = 0;
+  uint32_t h[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const uint64_t v = finite ? mul2(pack2(bf16_lo(ww[n]), bf16_hi(ww[n])), scale2) : 0;
+    float lo, hi;
+    unpack2(v, lo, hi);
+    s2 = n == 0 ? v : add2(s2, v);
+    h[n] = cvt_f16x2(lo, hi);
+  }
+#pragma unroll
+  for (int n = 0; n < kPieces; ++n) {
+    const uint32_t a = __byte_perm(h[0], h[1], 0x7351), b = __byte_perm(h[2], h[3], 0x7351);
+    *reinterpret_cast<uint2*>(to + n * piece_bytes) =
+        make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[q] = sub_f16x2(h[q], h[q] & 0xff00ff00u);
+  }
+  float lo, hi;
+  unpack2(s2, lo, hi);
+  sum = 0x1p-9f * (lo + hi);
+  for (int o = 1; o < group_lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+}
+// Offset of chunk c8 (eight columns) of token t in a piece.
+__device__ __forceinline__ int x_chunk(int t, int c8) {
+  return t * 128 + ((c8 / 2) ^ (t & 7)) * 16 + c8 % 2 * 8;
+}
+
+// x, split, for blocks of more than eight tokens: a warp for 256 columns of a row.
+// Layer: the rows of the pairs in sorted_ids, row pair / k of x.
 __global__ void __launch_bounds__(kSplitThreads)
     w4_split_kernel(const __nv_bfloat16* __restrict__ x, int T, int K, int nt, int group,
                     uint8_t* __restrict__ xq, const int32_t* __restrict__ sorted_ids,
                     const int32_t* __restrict__ num_padded, int P, int k) {
-  __shared__ float s_max[kSplitThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int block = blockIdx.x / nt, t = blockIdx.x % nt;
-  long long row = blockIdx.x;
+  const int steps = (K + kStepK - 1) / kStepK, lane = threadIdx.x % 32;
+  const long long item = blockIdx.x * (kSplitThreads / 32ll) + threadIdx.x / 32;
+  const long long at = item / steps;
+  const int step = static_cast<int>(item - at * steps);
+  long long row = at;
   if (sorted_ids != nullptr) {
-    if (row >= __ldg(num_padded)) return;
-    const int pair = __ldg(sorted_ids + row);
+    if (at >= __ldg(num_padded)) return;
+    const int pair = __ldg(sorted_ids + at);
     if (pair >= P) return;
     row = pair / k;
-  } else if (row >= T) {
+  } else if (at >= T) {
     return;
   }
   const XLayout lay(K, nt, group);
-  const uint4* src = reinterpret_cast<const uint4*>(x + row * K);
-  uint8_t* to = xq + block * lay.bytes();
-  const int tid = threadIdx.x, n8 = K / 8;
-  constexpr int kKeep = 4;  // loads kept from the first pass
-  uint4 keep[kKeep];
-  uint32_t m = 0;
-  auto top = [&](const uint4& w) {
-    m = max_bf16x2(m, max_bf16x2(max_bf16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                                 max_bf16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-  };
-#pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    keep[i] = tid + i * kSplitThreads < n8 ? __ldg(src + tid + i * kSplitThreads) : make_uint4(0, 0, 0, 0);
-    top(keep[i]);
-  }
-  for (int i = tid + kKeep * kSplitThreads; i < n8; i += kSplitThreads) top(__ldg(src + i));
-  m = max_bf16x2(m, m >> 16 | m << 16);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  // (magnitudes as integers order like the numbers, NaN above all)
-  if (tid % 32 == 0) s_max[tid / 32] = __uint_as_float(m << 16);
-  __syncthreads();
-  uint32_t top_bits = 0;
-#pragma unroll
-  for (int i = 0; i < kSplitThreads / 32; ++i) top_bits = max(top_bits, __float_as_uint(s_max[i]));
-  const bool finite = top_bits < 0x7f800000u;
-  // biased exponent of the largest; at least 14, so that the scale stays finite
-  const int ex = max(finite ? static_cast<int>(top_bits >> 23) : 0, 14);
-  const float scale = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(141 - ex)
-  const uint64_t scale2 = pack2(scale, scale);
-  if (tid == 0)
-    reinterpret_cast<float*>(to + lay.factors())[t] =
-        finite ? __uint_as_float(static_cast<uint32_t>(ex - 5) << 23) : __int_as_float(0x7fc00000);
-  float* sums = reinterpret_cast<float*>(to + lay.sums());
-  const int n8_pad = lay.n_cols * (kBlockK / 8);
-#pragma unroll 1
-  for (int i = tid; i < n8_pad; i += kSplitThreads) {  // whole half warps: a block is 16 threads
-    uint4 w = i < n8 && finite ? (i < kSplitThreads       ? keep[0]
-                                  : i < 2 * kSplitThreads ? keep[1]
-                                  : i < 3 * kSplitThreads ? keep[2]
-                                  : i < 4 * kSplitThreads ? keep[3]
-                                                   : __ldg(src + i))
-                               : make_uint4(0, 0, 0, 0);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    float sum = 0.f;
-    uint32_t h[4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      float lo, hi;
-      unpack2(mul2(pack2(bf16_lo(ww[n]), bf16_hi(ww[n])), scale2), lo, hi);
-      sum += lo + hi;
-      h[n] = cvt_f16x2(lo, hi);
-    }
-    const int blk = i / 16, c8 = i % 16;
-    uint8_t* p = to + static_cast<size_t>(blk) * kPieces * x_piece_bytes(nt) + t * 128 +
-                 ((c8 / 2) ^ (t & 7)) * 16 + c8 % 2 * 8;
-#pragma unroll
-    for (int n = 0; n < kPieces; ++n) {
-      const uint32_t a = __byte_perm(h[0], h[1], 0x7351), b = __byte_perm(h[2], h[3], 0x7351);
-      *reinterpret_cast<uint2*>(p + n * x_piece_bytes(nt)) =
-          make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-#pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = sub_f16x2(h[q], h[q] & 0xff00ff00u);
-    }
-    const unsigned half = 0xffffu << (tid & 16);
-    for (int o = 1; o < group / 8; o <<= 1) sum += __shfl_xor_sync(half, sum, o);
-    if (c8 % (group / 8) == 0)
-      sums[static_cast<size_t>(blk) * lay.per_block + c8 / (group / 8) * nt + t] = 0x1p-9f * sum;
-  }
+  const int t = static_cast<int>(at % nt), blk = 2 * step + lane / 16, c8 = lane % 16;
+  uint8_t* to = xq + at / nt * lay.bytes();
+  const int c = step * 32 + lane;
+  const uint4 w = c < K / 8 ? __ldg(reinterpret_cast<const uint4*>(x + row * K) + c) : make_uint4(0, 0, 0, 0);
+  float sum, factor;
+  split_columns(w, group / 8, to + static_cast<size_t>(blk) * kPieces * x_piece_bytes(nt) + x_chunk(t, c8),
+                x_piece_bytes(nt), sum, factor);
+  float* side = reinterpret_cast<float*>(to + lay.sides() + static_cast<size_t>(blk) * lay.side) + t;
+  if (c8 % (group / 8) == 0) side[c8 / (group / 8) * nt] = sum;
+  if (c8 == 0) side[kBlockK / group * nt] = factor;
 }
 
 enum W4Mode { kMatvec, kGateUp, kDown };
@@ -228,6 +226,7 @@ struct W4Job {
   int whole_stages;  // K % kStepK == 0 and aligned tensors: a stage's scales in one load
   int mode, K;
   int n_rows;    // rows of the result: N, I or H
+  int row_tiles; // tiles of them, kRows a thread block's (kRows / 2, gate/up)
   int n_blocks;  // blocks of tokens (an upper bound for the layer)
   const uint8_t* xq;        // x (down: h), split: an XLayout for each block of tokens
   const __nv_bfloat16* x;   // tokens (down: h by pair)
@@ -235,6 +234,7 @@ struct W4Job {
   void* out;     // matvec: [T][N]; gate/up: h bf16 [pair][I]; down: y fp32 [pair][H]
   int out_fp32;
   int cluster;   // thread blocks that split K
+  int stages;    // of codes
   // layer
   const int32_t* sorted_ids;
   const int32_t* block_expert;
@@ -247,7 +247,7 @@ struct W4Job {
 template <int PG, int NT>
 struct W4Shape {
   static constexpr int kN = NT < 16 ? 16 : NT;  // MMA N (16 at least with 128 rows)
-  static constexpr int kPerSm = NT == 8 ? 4 : NT == 16 ? 3 : 2;
+  static constexpr int kPerSm = NT <= 16 ? 3 : 2;
   static constexpr int kTmem = NT <= 16 ? 128 : 256;  // columns of tensor memory
   // Columns of a unit, what is multiplied at a time: as many as leave room for
   // two buffers of A and two sets of accumulators (one is read during the next
@@ -258,12 +258,13 @@ struct W4Shape {
   static constexpr int kUnits = kBlockK / kUnitK;  // of a block of columns
   static constexpr int kSub = kUnitK / (32 * PG);  // groups, so accumulators, of a unit
   static constexpr int kACols = kUnitK / 4;
-  static constexpr int kStages = NT == 8 ? 2 : 3;
   static constexpr int kXBytes = kPieces * x_piece_bytes(NT);
-  static constexpr int kSumSlots = kStages + 1;              // stages' sums of x
-  static constexpr int kSumBytes = 2 * (4 / PG) * NT * 4;    // of the two blocks of a stage
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes +
-                                  kXSlots * kXBytes + kSumSlots * kSumBytes;
+  static constexpr int kSideBytes = 2 * x_side_bytes(NT, 32 * PG);  // of a stage
+  static constexpr int kStageBytes = kCodeBytes + 2 * kXBytes;
+  // shared memory with so many stages (a stage's sides are read a little longer)
+  static constexpr int smem(int stages) {
+    return 1024 + stages * kStageBytes + (stages + 1) * kSideBytes + kRedBytes;
+  }
 };
 
 // sum_k x[k] (code[k] - zero) * scale over columns k0 .. k1 of a weight row,
@@ -289,49 +290,37 @@ __device__ __noinline__ float w4_row_plain(const W4Job& j, int group, size_t gro
 }
 
 // PG: 32-column pieces of a group (1, 2, 4).  NT: tokens of a block at most.
+// A cluster (of one block, where there are more jobs than clusters) takes every
+// gridDim.x / j.cluster-th job: a tile of rows for a block of tokens.
 template <int PG, bool ZP, int NT>
 __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     w4_kernel(const __grid_constant__ CUtensorMap map, const W4Job j) {
   using S = W4Shape<PG, NT>;
-  constexpr int kStages = S::kStages;
+  constexpr int kMmaThreads = kRowThreads + 32;  // at the barriers of A
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_codes[kStages];  // a stage's codes and sums of x are there
-  __shared__ uint64_t s_x[kXSlots];      // a block of x is there
-  __shared__ uint64_t s_done[2];         // even and odd units' MMAs are done
+  __shared__ uint64_t s_full[kMaxStages];   // a stage's codes and x are there
+  __shared__ uint64_t s_free[kMaxStages];   // and done with
+  __shared__ uint64_t s_done[2];            // even and odd units' MMAs are done
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  uint8_t* x_pieces = smem + kStages * kStageBytes;
-  float* x_sums = reinterpret_cast<float*>(x_pieces + kXSlots * S::kXBytes);
+  uint8_t* sides = smem + j.stages * S::kStageBytes;
+  float* s_red = reinterpret_cast<float*>(sides + (j.stages + 1) * S::kSideBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int CS = j.cluster;
   const int rank = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const bool layer = j.mode != kMatvec, gate_up = j.mode == kGateUp;
+  // The kernel before splits x, and waited itself for those before it: the weights and
+  // the lists of the alignment are older than it and are read before pdl_wait().
+  const int n_blocks = layer ? __ldcg(j.num_padded) / NT : j.n_blocks;
+  const int n_jobs = n_blocks * j.row_tiles;
+  const int job0 = static_cast<int>(blockIdx.x) / CS, job_step = static_cast<int>(gridDim.x) / CS;
+  if (job0 >= n_jobs) return;  // (all of its cluster does)
   if (tid == 0) {
     prefetch_tensormap(&map);
-    for (int i = 0; i < kStages; ++i) mbar_init(&s_codes[i], 1);
-    for (int i = 0; i < kXSlots; ++i) mbar_init(&s_x[i], 1);
+    for (int i = 0; i < j.stages; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_free[i], 1);
     mbar_init(&s_done[0], 1);
     mbar_init(&s_done[1], 1);
-    s_abort = 0;
     fence_mbarrier_init();
-  }
-  // Up to pdl_wait() nothing is read that the kernel before, which splits x, writes:
-  // the weights and the lists of the alignment are older than it.
-
-  // which rows and tokens; a block past the layer's last one leaves (all of its
-  // cluster does)
-  const int job = static_cast<int>(blockIdx.x) / CS;
-  const int block = job % j.n_blocks;
-  const int rows_out = j.mode == kGateUp ? kRows / 2 : kRows;  // rows of the result
-  const int r0 = job / j.n_blocks * rows_out;
-  int e = 0, valid;
-  if (j.mode == kMatvec) {
-    valid = min(NT, j.T - block * NT);
-  } else {
-    if (block * NT >= __ldg(j.num_padded)) return;
-    e = __ldg(j.block_expert + block);
-    const int32_t* ids = j.sorted_ids + static_cast<size_t>(block) * NT;
-    valid = __popc(__ballot_sync(0xffffffffu, lane < NT && __ldg(ids + min(lane, NT - 1)) < j.P));
   }
   if (warp == 4) {
     tmem_alloc(&s_tmem, S::kTmem);
@@ -340,7 +329,24 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = s_tmem, t_d = tmem + 2 * S::kACols;
-  const size_t expert_row = static_cast<size_t>(e) * j.n_rows * (j.mode == kGateUp ? 2 : 1);
+
+  // a job's rows of the result, and the expert (layer) that they are of
+  const int rows_out = gate_up ? kRows / 2 : kRows;
+  auto job_row = [&](int job) { return job / n_blocks * rows_out; };
+  auto job_expert = [&](int job) {
+    return layer && job < n_jobs ? __ldcg(j.block_expert + job % n_blocks) : 0;
+  };
+  // lane t: token t's pair (matvec: token), and how many there are
+  auto job_pair = [&](int job) {
+    const int at = job % n_blocks * NT + lane;
+    if (!layer) return at;
+    return lane < NT && job < n_jobs ? __ldcg(j.sorted_ids + at) : j.P;
+  };
+  const int pair_end = layer ? j.P : j.T;
+  auto count = [&](int pair) {
+    return __popc(__ballot_sync(0xffffffffu, lane < NT && pair < pair_end));
+  };
+  const int expert_rows = gate_up ? 2 * j.n_rows : j.n_rows;
 
   // this block's slice of K, in stages and blocks of columns
   const int all_steps = (j.K + kStepK - 1) / kStepK;
@@ -349,111 +355,158 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
   const int n_steps = step1 - step0;
   const int k0 = step0 * kStepK, k1 = min(step1 * kStepK, j.K);
   const int n_blks = (k1 - k0 + kBlockK - 1) / kBlockK;
-  // this thread's weight row (past the result's last one: that one)
-  const int row = tid % kRows;
-  const size_t grow = expert_row + min(r0 + row % rows_out, j.n_rows - 1) +
-                      (j.mode == kGateUp && row >= rows_out ? j.n_rows : 0);
 
   float acc[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = 0.f;
   bool ok = true;  // once a wait gives up, the loops run out without waits and MMAs
+  int my_row = 0, my_valid = 0, my_pair = 0;  // workers: of the last job
+  float my_weight = 0.f;
 
-  if (warp == 4) {
-    // ---------------------------------------------------------- copies and MMAs
-    const XLayout lay(j.K, NT, 32 * PG);
-    const uint8_t* xq = j.xq + block * lay.bytes();
-    auto issue_codes = [&](int step) {
-      uint64_t* bar = &s_codes[step % kStages];
-      uint8_t* dst = smem + step % kStages * kStageBytes;
-      mbar_arrive_expect_tx(bar, kStageBytes + S::kSumBytes);
-      const int col = (step0 + step) * (kStepK / 2), row_a = static_cast<int>(expert_row) + r0;
-      tma_load_2d(dst, &map, bar, col, row_a);
-      tma_load_2d(dst + kStageBytes / 2, &map, bar, col,
-                  row_a + (j.mode == kGateUp ? j.n_rows : kRows / 2));
-    };
-    auto issue_sums = [&](int step) {
-      bulk_load(x_sums + step % S::kSumSlots * (S::kSumBytes / 4),
-                xq + lay.sums() + static_cast<size_t>(step0 + step) * S::kSumBytes, S::kSumBytes,
-                &s_codes[step % kStages]);
-    };
-    const int x_rows = (valid + 7) / 8 * 8;
-    auto issue_x = [&](int blk) {
-      uint64_t* bar = &s_x[blk % kXSlots];
-      uint8_t* dst = x_pieces + blk % kXSlots * S::kXBytes;
-      const uint8_t* src = xq + static_cast<size_t>(k0 / kBlockK + blk) * S::kXBytes;
-      mbar_arrive_expect_tx(bar, kPieces * x_rows * 128);
-      if (x_rows == NT) {
-        bulk_load(dst, src, S::kXBytes, bar);
+  // Results from sums in shared memory, [token][row] from token t0 on, each the sum of
+  // `ranks` blocks' (in that order), `part` of the `of` parts of them.
+  auto store = [&](const float* red, int t0, int n_tokens, int part, int of) {
+    const uint32_t red_at = smem_addr(red);
+    for (int i = part * kRowThreads + tid; i < rows_out * n_tokens; i += of * kRowThreads) {
+      const int t = i / rows_out, r = i % rows_out;
+      const int pair = __shfl_sync(0xffffffffu, my_pair, t0 + t);
+      const float weight = __shfl_sync(0xffffffffu, my_weight, t0 + t);
+      float v = 0.f, up = 0.f;
+      if (CS == 1) {
+        v = red[t * kRows + r];
+        if (gate_up) up = red[t * kRows + kRows / 2 + r];
       } else {
-        for (int n = 0; n < kPieces; ++n)
-          bulk_load(dst + n * x_piece_bytes(NT), src + n * x_piece_bytes(NT), x_rows * 128, bar);
+        for (int c = 0; c < CS; ++c) {
+          v += ld_cluster_f32(mapa_shared(red_at + (t * kRows + r) * 4, c));
+          if (gate_up) up += ld_cluster_f32(mapa_shared(red_at + (t * kRows + kRows / 2 + r) * 4, c));
+        }
       }
-    };
-    int codes_issued = min(kStages, n_steps), x_issued = min(kXSlots, n_blks);
-    if (elect_one())
-      for (int i = 0; i < codes_issued; ++i) issue_codes(i);
-    __syncwarp();
-    pdl_wait();
-    pdl_trigger();
-    if (elect_one()) {
-      for (int i = 0; i < codes_issued; ++i) issue_sums(i);
-      for (int i = 0; i < x_issued; ++i) issue_x(i);
+      if (my_row + r >= j.n_rows) continue;
+      const size_t o = static_cast<size_t>(pair) * j.n_rows + my_row + r;
+      if (gate_up) v = v / (1.f + expf(-v)) * up;
+      if (j.mode == kDown) v *= weight;
+      if (j.out_fp32) static_cast<float*>(j.out)[o] = v;
+      else static_cast<__nv_bfloat16*>(j.out)[o] = __float2bfloat16_rn(v);
     }
-    __syncwarp();
-    // N: the block's tokens, and eight stand for both eight-row halves of 16
-    const uint32_t idesc = w4_idesc(max(16, (valid + 15) / 16 * 16));
-    const uint64_t db0 = sdesc_kmajor_sw128(smem_addr(x_pieces)) -
-                         (NT == 8 ? static_cast<uint64_t>(1024 >> 4) << 32 : 0);
-    for (int blk = 0; blk < n_blks; ++blk) {
-      ok = ok && warp_wait(&s_x[blk % kXSlots], blk / kXSlots & 1);
-#pragma unroll
-      for (int h = 0; h < S::kUnits; ++h) {
-        const int u = blk * S::kUnits + h;
-        named_barrier(1 + (u & 1), kThreads);  // A is in place
-        if (ok && elect_one()) {
-          tc_fence_after_sync();
-          const uint64_t db = db0 + blk % kXSlots * (S::kXBytes / 16);
-          const uint32_t a = tmem + (u & 1) * S::kACols;
-          const uint32_t d = t_d + (u & 1) * (S::kN * S::kSub);
-#pragma unroll
-          for (int n = kPieces - 1; n >= 0; --n)  // small pieces first
-#pragma unroll
-            for (int i = 0; i < S::kUnitK / 32; ++i)
-              umma_f8_ts(d + i / PG * S::kN, a + i * 8,
-                         db + n * (x_piece_bytes(NT) / 16) + (h * (S::kUnitK / 32) + i) * 2, idesc,
-                         n < kPieces - 1 || i % PG != 0);
-          umma_commit(&s_done[u & 1]);
-        }
-        __syncwarp();
-      }
-      // Every warp has read the block's codes, and has added the sums of the block
-      // before the last: a stage is free after its second block, and x's buffer of
-      // two blocks ago too.
-      if (ok && elect_one()) {
-        if (blk % 2 == 1 && codes_issued < n_steps) {
-          issue_codes(codes_issued);
-          issue_sums(codes_issued);
-        }
-        if (blk >= 2 && x_issued < n_blks) issue_x(x_issued);
+  };
+
+  if (warp == 5) {
+    // ---------------------------------------------------------- copies
+    // The next stage, of this job or one to come: its codes, and what comes after
+    // pdl_wait(), its x.
+    int c_job = job0, c_step = 0, c_slot = 0, c_count = 0, c_row, c_next_expert;
+    c_row = job_expert(c_job) * expert_rows + job_row(c_job);
+    c_next_expert = job_expert(c_job + job_step);
+    const int x_rows = layer ? NT : min(NT, (j.T + 7) / 8 * 8);
+    auto issue_codes = [&]() {
+      if (c_job >= n_jobs) return;
+      if (elect_one()) {
+        uint64_t* bar = &s_full[c_slot];
+        uint8_t* dst = smem + c_slot * S::kStageBytes;
+        mbar_arrive_expect_tx(bar, kCodeBytes + 2 * kPieces * x_rows * 128 + S::kSideBytes);
+        const int col = (step0 + c_step) * (kStepK / 2);
+        tma_load_2d(dst, &map, bar, col, c_row);
+        tma_load_2d(dst + kCodeBytes / 2, &map, bar, col, c_row + (gate_up ? j.n_rows : kRows / 2));
       }
       __syncwarp();
-      if (blk % 2 == 1 && codes_issued < n_steps) ++codes_issued;
-      if (blk >= 2 && x_issued < n_blks) ++x_issued;
+      ++c_count;
+      if (++c_slot == j.stages) c_slot = 0;
+      if (++c_step == n_steps) {
+        c_step = 0;
+        c_job += job_step;
+        c_row = c_next_expert * expert_rows + job_row(c_job);
+        c_next_expert = job_expert(c_job + job_step);
+      }
+    };
+    const XLayout lay(j.K, NT, 32 * PG);
+    int x_job = job0, x_step = 0, x_slot = 0, side_slot = 0;
+    const uint8_t* xq = j.xq + x_job % n_blocks * lay.bytes();
+    auto issue_x = [&]() {
+      if (x_job >= n_jobs) return;
+      if (elect_one()) {
+        uint64_t* bar = &s_full[x_slot];
+        uint8_t* dst = smem + x_slot * S::kStageBytes + kCodeBytes;
+        const size_t step = step0 + x_step;
+        const uint8_t* src = xq + step * (2 * S::kXBytes);
+        if (x_rows == NT) {
+          bulk_load(dst, src, 2 * S::kXBytes, bar);
+        } else {
+          for (int n = 0; n < 2 * kPieces; ++n)
+            bulk_load(dst + n * x_piece_bytes(NT), src + n * x_piece_bytes(NT), x_rows * 128, bar);
+        }
+        bulk_load(sides + side_slot * S::kSideBytes, xq + lay.sides() + step * S::kSideBytes,
+                  S::kSideBytes, bar);
+      }
+      __syncwarp();
+      if (++x_slot == j.stages) x_slot = 0;
+      if (++side_slot == j.stages + 1) side_slot = 0;
+      if (++x_step == n_steps) {
+        x_step = 0;
+        x_job += job_step;
+        xq = j.xq + x_job % n_blocks * lay.bytes();
+      }
+    };
+    for (int i = 0; i < j.stages; ++i) issue_codes();
+    pdl_wait();
+    pdl_trigger();
+    for (int i = 0; i < j.stages; ++i) issue_x();
+    int slot = 0, phase = 0;
+    while (c_job < n_jobs) {
+      ok = warp_wait(&s_free[slot], phase);
+      if (!ok) break;
+      issue_codes();
+      issue_x();
+      if (++slot == j.stages) slot = 0, phase ^= 1;
     }
     if (!ok) {  // the copies in flight land before the block leaves
-      for (int i = max(0, codes_issued - kStages); i < codes_issued; ++i)
-        warp_wait(&s_codes[i % kStages], i / kStages & 1);
-      for (int i = max(0, x_issued - kXSlots); i < x_issued; ++i)
-        warp_wait(&s_x[i % kXSlots], i / kXSlots & 1);
+      for (int i = max(0, c_count - j.stages); i < c_count; ++i)
+        warp_wait(&s_full[i % j.stages], i / j.stages & 1);
+    }
+  } else if (warp == 4) {
+    // ---------------------------------------------------------- MMAs
+    // (N: eight tokens stand for both eight-row halves of 16)
+    constexpr uint32_t idesc = w4_idesc(S::kN);
+    const uint64_t db0 = sdesc_kmajor_sw128(smem_addr(smem + kCodeBytes)) -
+                         (NT == 8 ? static_cast<uint64_t>(1024 >> 4) << 32 : 0);
+    int u = 0, slot = 0, phase = 0;
+    for (int job = job0; job < n_jobs; job += job_step) {
+      for (int blk = 0; blk < n_blks; ++blk) {
+        if (blk % 2 == 0) ok = ok && warp_wait(&s_full[slot], phase);
+        const bool last = blk % 2 == 1 || blk == n_blks - 1;  // of its stage
+#pragma unroll
+        for (int h = 0; h < S::kUnits; ++h, u ^= 1) {
+          named_barrier(1 + u, kMmaThreads);  // A is in place
+          if (ok && elect_one()) {
+            tc_fence_after_sync();
+            const uint64_t db = db0 + slot * (S::kStageBytes / 16) + blk % 2 * (S::kXBytes / 16);
+            const uint32_t a = tmem + u * S::kACols;
+            const uint32_t d = t_d + u * (S::kN * S::kSub);
+#pragma unroll
+            for (int n = kPieces - 1; n >= 0; --n)  // small pieces first
+#pragma unroll
+              for (int i = 0; i < S::kUnitK / 32; ++i)
+                umma_f8_ts(d + i / PG * S::kN, a + i * 8,
+                           db + n * (x_piece_bytes(NT) / 16) + (h * (S::kUnitK / 32) + i) * 2,
+                           idesc, n < kPieces - 1 || i % PG != 0);
+            umma_commit(&s_done[u]);
+            // (every warp has read the stage's codes, and the sides of the one before)
+            if (last && h == S::kUnits - 1) umma_commit(&s_free[slot]);
+          }
+          __syncwarp();
+        }
+        if (last && ++slot == j.stages) slot = 0, phase ^= 1;
+      }
     }
   } else {
     // ---------------------------------------------------------- codes and sums
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const int groups = (j.K + 32 * PG - 1) / (32 * PG);
-    const size_t group0 = grow * groups + k0 / (32 * PG);
-    // the row's scales and zero points of this slice on their way to L2
-    {
+    constexpr int kGroups = 8 / PG, kBlkGroups = 4 / PG;
+    size_t grow, group0;  // this thread's weight row, and its first group in this slice of K
+    auto find_row = [&](int job) {
+      const int r0 = job_row(job);  // past the result's last row: that one
+      grow = static_cast<size_t>(job_expert(job)) * expert_rows + min(r0 + tid % rows_out, j.n_rows - 1) +
+             (tid >= rows_out ? j.n_rows : 0);
+      group0 = grow * groups + k0 / (32 * PG);
+      // its scales and zero points on their way to L2
       const int n = (k1 - k0 + 32 * PG - 1) / (32 * PG), lg = j.scale_bf16 ? 1 : 2;
       const uint8_t* p = static_cast<const uint8_t*>(j.scales) + (group0 << lg);
       for (int i = 0; i < n << lg; i += 128) prefetch_l2(p + i);
@@ -462,15 +515,13 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
         for (int i = 0; i < n; i += 128) prefetch_l2(j.zeros + group0 + i);
         prefetch_l2(j.zeros + group0 + n - 1);
       }
-    }
+    };
     // Scales and zero points of a stage's groups, as they lie in memory: one load
     // each when every row's stage starts on its size (K a multiple of the stage's
     // columns), else group by group.
-    constexpr int kGroups = 8 / PG;
     uint32_t s_raw[kGroups], z_raw[(kGroups + 3) / 4];
     auto fetch_scales = [&](int step) {
       const size_t at = group0 + static_cast<size_t>(step) * kGroups;
-      if (step >= n_steps) return;
       if (j.whole_stages) {
         if (j.scale_bf16) {
           const uint8_t* p = static_cast<const uint8_t*>(j.scales) + at * 2;
@@ -507,56 +558,51 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     };
 #pragma unroll
     for (int i = 0; i < (kGroups + 3) / 4; ++i) z_raw[i] = 0;
+    find_row(job0);
     fetch_scales(0);
-    constexpr int kBlkGroups = 4 / PG;
     float s_step[kGroups], s_old[S::kSub], z_old[S::kSub];
     uint32_t z_step[(kGroups + 3) / 4];
-    const float* sums_old = x_sums;  // of the last unit's groups
-    // adds unit u's sums, scaled
-    auto flush = [&](int u) {
-      float4 xs[NT <= 8 ? S::kSub : 1][2];
-      if (NT <= 8) {
-#pragma unroll
-        for (int i = 0; i < S::kSub; ++i) {
-          xs[i][0] = *reinterpret_cast<const float4*>(sums_old + i * NT);
-          xs[i][1] = *reinterpret_cast<const float4*>(sums_old + i * NT + 4);
-        }
-      }
-      ok = ok && warp_wait(&s_done[u & 1], u >> 1 & 1);
+    // the unit to come (even or odd, and its barrier's phase)
+    int u = 0, u_phase = 0;
+    const float *sums_old = nullptr, *factors_old = nullptr;  // of the last unit
+    // adds the last unit's sums, scaled
+    auto flush = [&]() {
+      const int v = u ^ 1, v_phase = u_phase ^ v;
+      ok = ok && warp_wait(&s_done[v], v_phase);
       tc_fence_after_sync();
-      const uint32_t at = t_d + lanes + (u & 1) * (S::kN * S::kSub);
+      const uint32_t at = t_d + lanes + v * (S::kN * S::kSub);
 #pragma unroll
       for (int t0 = 0; t0 < NT; t0 += 8) {
-        if (t0 > 0 && t0 >= valid) break;
+        if (t0 > 0 && t0 >= my_valid) break;
         uint32_t d[S::kSub][8];
 #pragma unroll
         for (int i = 0; i < S::kSub; ++i) tmem_ld8_async(at + i * S::kN + t0, d[i]);
+        const float4 f[2] = {*reinterpret_cast<const float4*>(factors_old + t0),
+                             *reinterpret_cast<const float4*>(factors_old + t0 + 4)};
 #pragma unroll
         for (int i = 0; i < S::kSub; ++i) {
           tmem_wait_ld8(d[i]);
           const uint64_t zz = pack2(-z_old[i], -z_old[i]), ss = pack2(s_old[i], s_old[i]);
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            const float4 xv = NT <= 8 ? xs[i][n / 2]
-                                      : *reinterpret_cast<const float4*>(sums_old + i * NT + t0 +
-                                                                         n / 2 * 4);
+            const float4 xv = *reinterpret_cast<const float4*>(sums_old + i * NT + t0 + n / 2 * 4);
             const uint64_t x2 = n % 2 ? pack2(xv.z, xv.w) : pack2(xv.x, xv.y);
+            const uint64_t f2 = n % 2 ? pack2(f[n / 2].z, f[n / 2].w) : pack2(f[n / 2].x, f[n / 2].y);
             const uint64_t d2 =
                 pack2(__uint_as_float(d[i][2 * n]), __uint_as_float(d[i][2 * n + 1]));
             float& lo = acc[t0 + 2 * n];
             float& hi = acc[t0 + 2 * n + 1];
-            unpack2(fma2(ss, fma2(zz, x2, d2), pack2(lo, hi)), lo, hi);
+            unpack2(fma2(mul2(ss, f2), fma2(zz, x2, d2), pack2(lo, hi)), lo, hi);
           }
         }
       }
     };
     // a block of 128 columns, the hb-th of its stage
-    auto columns = [&](int blk, int slot, const float* sums, auto which) {
+    auto columns = [&](int slot, const float* side, bool first, auto which) {
       constexpr int hb = decltype(which)::value;
-      const uint8_t* codes = smem + slot * kStageBytes + tid * 128;
+      const uint8_t* codes = smem + slot * S::kStageBytes + tid * 128;
 #pragma unroll
       for (int h = 0; h < S::kUnits; ++h) {
-        const int u = blk * S::kUnits + h;
         uint32_t v[S::kACols];
 #pragma unroll
         for (int c = 0; c < S::kUnitK / 32; ++c) {
@@ -570,118 +616,103 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
           }
         }
         // the MMAs that read this buffer of A were waited for when their sums were added
-        const uint32_t a = tmem + (u & 1) * S::kACols + lanes;
+        const uint32_t a = tmem + u * S::kACols + lanes;
 #pragma unroll
         for (int n = 0; n < S::kACols; n += 16) tmem_st16(a + n, v + n);
         tmem_wait_st();
         tc_fence_before_sync();
         // A is in place, and the unit's codes are read.  (After a wait that gave up
         // nothing but this barrier keeps the warps together.)
-        if (ok) named_barrier_arrive(1 + (u & 1), kThreads);
-        else named_barrier(1 + (u & 1), kThreads);
-        if (u > 0) flush(u - 1);
+        if (ok) named_barrier_arrive(1 + u, kMmaThreads);
+        else named_barrier(1 + u, kMmaThreads);
+        if (!(first && hb == 0 && h == 0)) flush();
 #pragma unroll
         for (int i = 0; i < S::kSub; ++i) {
           const int g = hb * kBlkGroups + h * S::kSub + i;
           s_old[i] = s_step[g];
           z_old[i] = ZP ? static_cast<float>(z_step[g / 4] >> (8 * (g % 4)) & 0xffu) : 8.f;
         }
-        sums_old = sums + (hb * kBlkGroups + h * S::kSub) * NT;
+        const float* block_side = side + hb * (4 / PG + 1) * NT;
+        sums_old = block_side + h * S::kSub * NT;
+        factors_old = block_side + 4 / PG * NT;
+        u ^= 1;
+        u_phase ^= u ^ 1;
       }
     };
-    int slot = 0, phase = 0, sum_slot = 0;
-    for (int step = 0; step < n_steps; ++step) {
+    int slot = 0, phase = 0, side_slot = 0;
+    for (int job = job0; job < n_jobs; job += job_step) {
+      my_row = job_row(job), my_pair = job_pair(job), my_valid = count(my_pair);
+      if (j.mode == kDown) my_weight = lane < my_valid ? __ldcg(j.wts + my_pair) : 0.f;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i)
-        s_step[i] = __uint_as_float(!j.scale_bf16 ? s_raw[i]
-                                    : i % 2       ? s_raw[i / 2] & 0xffff0000u
-                                                  : s_raw[i / 2] << 16);
+      for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+      const size_t this_row = grow;
+      for (int step = 0; step < n_steps; ++step) {
 #pragma unroll
-      for (int i = 0; i < (kGroups + 3) / 4; ++i) z_step[i] = z_raw[i];
-      fetch_scales(step + 1);
-      ok = ok && warp_wait(&s_codes[slot], phase);
-      const float* sums = x_sums + sum_slot * (S::kSumBytes / 4);
-      columns(2 * step, slot, sums, std::integral_constant<int, 0>{});
-      if (2 * step + 1 < n_blks)
-        columns(2 * step + 1, slot, sums, std::integral_constant<int, 1>{});
-      if (++slot == kStages) slot = 0, phase ^= 1;
-      if (++sum_slot == S::kSumSlots) sum_slot = 0;
-    }
-    flush(n_blks * S::kUnits - 1);
-    pdl_wait();  // (what follows reads what the kernel before wrote, without a barrier)
-    {
-      const XLayout lay(j.K, NT, 32 * PG);
-      const float* factors = reinterpret_cast<const float*>(j.xq + block * lay.bytes() + lay.factors());
+        for (int i = 0; i < kGroups; ++i)
+          s_step[i] = __uint_as_float(!j.scale_bf16 ? s_raw[i]
+                                      : i % 2       ? s_raw[i / 2] & 0xffff0000u
+                                                    : s_raw[i / 2] << 16);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (t < valid) acc[t] *= __ldg(factors + t);
-    }
-    // a sum that is not a number: as the weights and tokens have it, column by column
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (t < valid && isnan(acc[t])) {
-        size_t at = static_cast<size_t>(block) * NT + t;
-        if (j.mode != kMatvec) {
-          const int pair = __ldg(j.sorted_ids + at);
-          at = static_cast<size_t>(j.mode == kGateUp ? pair / j.k : pair);
+        for (int i = 0; i < (kGroups + 3) / 4; ++i) z_step[i] = z_raw[i];
+        if (step + 1 < n_steps) {
+          fetch_scales(step + 1);
+        } else if (job + job_step < n_jobs) {
+          find_row(job + job_step);
+          fetch_scales(0);
         }
-        acc[t] = w4_row_plain(j, 32 * PG, grow, j.x + at * j.K, k0, k1);
+        ok = ok && warp_wait(&s_full[slot], phase);
+        const float* side = reinterpret_cast<const float*>(sides + side_slot * S::kSideBytes);
+        columns(slot, side, step == 0, std::integral_constant<int, 0>{});
+        if (2 * step + 1 < n_blks) columns(slot, side, false, std::integral_constant<int, 1>{});
+        if (++slot == j.stages) slot = 0, phase ^= 1;
+        if (++side_slot == j.stages + 1) side_slot = 0;
+      }
+      flush();
+      // Out through shared memory (a cluster's only job: through the stages' space).  A
+      // sum that is not a number: as the weights and tokens have it, column by column.
+#pragma unroll
+      for (int t0 = 0; t0 < NT; t0 += kRedTokens) {
+        if (t0 > 0 && t0 >= my_valid) break;
+        float* red = CS > 1 ? reinterpret_cast<float*>(smem) + t0 * kRows : s_red;
+        const int n_tokens = min(my_valid - t0, kRedTokens);
+        if (CS == 1) named_barrier(3, kRowThreads);  // the sums before are stored
+        bool nan = false;
+#pragma unroll
+        for (int t = 0; t < kRedTokens; ++t) {
+          red[t * kRows + tid] = ok ? acc[t0 + t] : __int_as_float(0x7fc00000);
+          nan = nan || (isnan(acc[t0 + t]) && t < n_tokens);
+        }
+        if (__any_sync(0xffffffffu, nan && ok)) {
+          pdl_wait();  // (x may come from the kernel before; no barrier was passed)
+#pragma unroll 1
+          for (int t = 0; t < n_tokens; ++t) {
+            const int pair = __shfl_sync(0xffffffffu, my_pair, t0 + t);
+            if (isnan(red[t * kRows + tid]))
+              red[t * kRows + tid] =
+                  w4_row_plain(j, 32 * PG, this_row,
+                               j.x + static_cast<size_t>(gate_up ? pair / j.k : pair) * j.K, k0, k1);
+          }
+        }
+        if (CS > 1) continue;
+        named_barrier(3, kRowThreads);
+        store(red, t0, n_tokens, 0, 1);
       }
     }
   }
-  if (!ok) s_abort = 1;
+  if (!ok && lane == 0 && j.err != nullptr) atomicOr(j.err, kDevErrTimeout);
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (s_abort) {
-    if (tid == 0 && j.err != nullptr) atomicOr(j.err, kDevErrTimeout);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = __int_as_float(0x7fc00000);  // a wrong sum shows
-  }
   if (warp == 4) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, S::kTmem);
   }
-  // the sums over the cluster's slices of K, in rank order, in the stages' space:
-  // red[token][row]
-  float* red = reinterpret_cast<float*>(smem);
-  if (warp < 4) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) red[t * kRows + tid] = acc[t];
-  }
+  if (CS == 1) return;
   __syncwarp();
-  if (CS > 1) cluster_sync();
-  else __syncthreads();
-  const uint32_t red_at = smem_addr(red);
-  auto sum = [&](int t, int r) {
-    if (CS == 1) return red[t * kRows + r];
-    float v = 0.f;
-    for (int i = 0; i < CS; ++i)
-      v += ld_cluster_f32(mapa_shared(red_at + (t * kRows + r) * 4, i));
-    return v;
-  };
-  for (int i = rank * kThreads + tid; i < rows_out * valid; i += CS * kThreads) {
-    const int t = i / rows_out, r = i % rows_out;
-    if (r0 + r >= j.n_rows) continue;
-    if (j.mode == kMatvec) {
-      const float v = sum(t, r);
-      const size_t o = (static_cast<size_t>(block) * NT + t) * j.n_rows + r0 + r;
-      if (j.out_fp32) static_cast<float*>(j.out)[o] = v;
-      else static_cast<__nv_bfloat16*>(j.out)[o] = __float2bfloat16_rn(v);
-    } else {
-      const int pair = __ldg(j.sorted_ids + static_cast<size_t>(block) * NT + t);
-      const size_t o = static_cast<size_t>(pair) * j.n_rows + r0 + r;
-      if (j.mode == kGateUp) {
-        const float gate = sum(t, r), up = sum(t, r + rows_out);
-        static_cast<__nv_bfloat16*>(j.out)[o] =
-            __float2bfloat16_rn(gate / (1.f + expf(-gate)) * up);
-      } else {
-        static_cast<float*>(j.out)[o] = __ldg(j.wts + pair) * sum(t, r);
-      }
-    }
-  }
+  cluster_sync();
+  if (warp < 4) store(reinterpret_cast<float*>(smem), 0, my_valid, rank, CS);
   __syncwarp();
-  if (CS > 1) cluster_sync();  // no block leaves while another reads its sums
+  cluster_sync();  // no block leaves while another reads its sums
 }
 
 // out[t] = sum of its k weighted rows, in slot order.
@@ -705,38 +736,64 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Thread blocks that split K: as many as there is room for at a time, each with a
-// stage at least.
+// Thread blocks that split K, a cluster: as many as leave the busiest SM the fewest
+// stages, of those that run at once.
 int choose_cluster(int K, long long tiles, int per_sm, int num_sms) {
   const int steps = (K + kStepK - 1) / kStepK;
-  int c = 1;
-  while (c < 8 && 2 * c <= steps && tiles * 2 * c <= static_cast<long long>(per_sm) * num_sms) c *= 2;
-  return c;
+  int best = 1;
+  long long least = -1;
+  for (int c = 1; c <= kMaxCluster && c <= steps; c *= 2) {
+    const long long blocks = tiles * c;
+    if (c > 1 && blocks > static_cast<long long>(per_sm) * num_sms) break;
+    const long long cost = (blocks + num_sms - 1) / num_sms * ((steps + c - 1) / c);
+    if (least < 0 || cost <= least) least = cost, best = c;
+  }
+  return best;
+}
+
+// What a kernel may use, set once for a device.
+cudaError_t allow(const void* kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = checked(cudaGetDevice(&dev), "current device");
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = checked(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem),
+              "smem attribute");
+  if (e == cudaSuccess)
+    e = checked(cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared),
+                "smem attribute");
+  if (e == cudaSuccess)
+    e = checked(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
+                "cluster attribute");
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 template <int PG, bool ZP, int NT>
 cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaStream_t st) {
   using S = W4Shape<PG, NT>;
-  cudaError_t e = checked(cudaFuncSetAttribute(w4_kernel<PG, ZP, NT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(S::kSmem)),
-                          "smem attribute");
-  if (e == cudaSuccess)
-    e = checked(cudaFuncSetAttribute(w4_kernel<PG, ZP, NT>,
-                                     cudaFuncAttributePreferredSharedMemoryCarveout,
-                                     cudaSharedmemCarveoutMaxShared),
-                "smem attribute");
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow(reinterpret_cast<const void*>(w4_kernel<PG, ZP, NT>), done);
   if (e != cudaSuccess) return e;
   W4Job j = job;
   j.whole_stages = j.K % kStepK == 0 && reinterpret_cast<uintptr_t>(j.scales) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(j.zeros) % 8 == 0;
   const int rows = j.mode == kGateUp ? kRows / 2 : kRows;
-  const long long tiles = (static_cast<long long>(j.n_rows) + rows - 1) / rows * j.n_blocks;
+  j.row_tiles = (j.n_rows - 1) / rows + 1;
+  const long long tiles = static_cast<long long>(j.row_tiles) * j.n_blocks;
   j.cluster = choose_cluster(j.K, tiles, S::kPerSm, num_sms);
+  const long long blocks = std::min(tiles * j.cluster, static_cast<long long>(S::kPerSm) * num_sms);
+  // As many stages as shared memory holds when the SMs share the blocks evenly.
+  const int steps = (j.K + kStepK - 1) / kStepK;
+  const int per_sm = j.cluster > 1 ? S::kPerSm : static_cast<int>((blocks + num_sms - 1) / num_sms);
+  j.stages = std::min(kMaxStages, (steps + j.cluster - 1) / j.cluster);
+  while (j.stages > 1 && S::smem(j.stages) + kStaticSmem > kSmSmem / per_sm) --j.stages;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * j.cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.dynamicSmemBytes = static_cast<size_t>(S::smem(j.stages));
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -793,9 +850,11 @@ namespace {
 cudaError_t launch_split(const __nv_bfloat16* x, int T, int K, int n_blocks, int nt, int group,
                          uint8_t* xq, const int32_t* sorted_ids, const int32_t* num_padded, int P,
                          int k, cudaStream_t st) {
-  return launch_pdl(w4_split_kernel, dim3(static_cast<unsigned>(n_blocks) * nt), dim3(kSplitThreads),
-                    0, st,
-                    x, T, K, nt, group, xq, sorted_ids, num_padded, P, k);
+
+  const long long warps = static_cast<long long>(n_blocks) * nt * ((K + kStepK - 1) / kStepK);
+  constexpr int kWarps = kSplitThreads / 32;
+  return launch_pdl(w4_split_kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)),
+                    dim3(kSplitThreads), 0, st, x, T, K, nt, group, xq, sorted_ids, num_padded, P, k);
 }
 
 }  // namespace
@@ -851,6 +910,7 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   if (e != cudaSuccess) return e;
   set_weight(j, p.w2);
   j.mode = kDown;
+  j.out_fp32 = 1;
   j.K = p.I;
   j.n_rows = p.H;
   j.xq = p.hq;
