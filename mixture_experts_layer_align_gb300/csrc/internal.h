@@ -184,10 +184,16 @@ struct W4LayerParams {
   const __nv_bfloat16* x;
   W4View w13, w2;
   int T, H, I, E, k;
-  const float* wts;             // [T*k] router weights
-  const int32_t* sorted_ids;    // pair ids by expert in blocks of w4_block_rows(T), T*k pads
-  const int32_t* block_expert;  // expert of each block
-  const int32_t* num_padded;    // rows of all blocks
+  const float* logits;          // [T][E]
+  int renorm;
+  // Written by launch_w4_layer where w4_front_fits(), else by the router and the
+  // alignment before it:
+  int32_t* ids;                 // [T*k] experts
+  float* wts;                   // [T*k] router weights
+  int32_t* counts;              // [E] pairs
+  int32_t* sorted_ids;          // pair ids by expert in blocks of w4_layer_block_rows(), T*k pads
+  int32_t* block_expert;        // expert of each block
+  int32_t* num_padded;          // rows of all blocks
   __nv_bfloat16* h;             // [T*k][I]
   uint8_t *xq, *hq;             // x and h of the blocks, split
   float* y;                     // [T*k][H]
@@ -197,6 +203,7 @@ struct W4LayerParams {
 // Rows of an alignment block: the pairs of one expert that one thread block takes.
 int w4_block_rows(int T);                       // matvec
 int w4_layer_block_rows(int T, int E, int k);   // layer
+bool w4_front_fits(int T, int E, int k);
 cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
                             const W4LayerParams& p, int num_sms, cudaStream_t st);
 

@@ -865,7 +865,8 @@ size_t moe_w4_workspace_size(int T, int H, int I, int E, int top_k) {
 
 int moe_w4_launch_count(int T, int H, int I, int E, int top_k) {
   if (!w4_sizes_ok(T, H, I, E, top_k) || !w4_sizes_supported(T, H, I, top_k)) return -1;
-  return T == 0 ? 0 : 7;  // router, alignment, split, gate/up, split, down, combine
+  // router, alignment and split, or a kernel for each; gate/up, split, down, combine
+  return T == 0 ? 0 : w4_front_fits(T, E, top_k) ? 5 : 7;
 }
 
 moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t workspace_bytes,
@@ -899,25 +900,31 @@ moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t worksp
   p.k = k;
   int32_t* ids = a->topk_ids_out ? a->topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
   float* wts = a->topk_w_out ? a->topk_w_out : reinterpret_cast<float*>(ws + L.wts);
-  if (launch_route_topk(a->router_logits, T, E, k, a->renormalize, ids, wts, nullptr, 0, nullptr,
-                        reinterpret_cast<Ctrl*>(ws + L.ctrl), nullptr, 0, stream) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  AlignParams ap{};
-  ap.ids = ids;
-  ap.P = T * k;
-  ap.E = E;
-  ap.bm = w4_layer_block_rows(T, E, k);
-  ap.chunk = align_chunk();
-  ap.counts = a->counts_out ? a->counts_out : reinterpret_cast<int32_t*>(ws + L.counts);
-  ap.offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
-  ap.sorted_ids = reinterpret_cast<int32_t*>(ws + L.sorted);
-  ap.tile_expert = reinterpret_cast<int32_t*>(ws + L.blocks);
-  ap.num_padded = reinterpret_cast<int32_t*>(ws + L.padded);
-  if (launch_align(ap, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  p.logits = a->router_logits;
+  p.renorm = a->renormalize;
+  p.ids = ids;
   p.wts = wts;
-  p.sorted_ids = ap.sorted_ids;
-  p.block_expert = ap.tile_expert;
-  p.num_padded = ap.num_padded;
+  p.counts = a->counts_out ? a->counts_out : reinterpret_cast<int32_t*>(ws + L.counts);
+  p.sorted_ids = reinterpret_cast<int32_t*>(ws + L.sorted);
+  p.block_expert = reinterpret_cast<int32_t*>(ws + L.blocks);
+  p.num_padded = reinterpret_cast<int32_t*>(ws + L.padded);
+  if (!w4_front_fits(T, E, k)) {
+    if (launch_route_topk(a->router_logits, T, E, k, a->renormalize, ids, wts, nullptr, 0, nullptr,
+                          reinterpret_cast<Ctrl*>(ws + L.ctrl), nullptr, 0, stream) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    AlignParams ap{};
+    ap.ids = ids;
+    ap.P = T * k;
+    ap.E = E;
+    ap.bm = w4_layer_block_rows(T, E, k);
+    ap.chunk = align_chunk();
+    ap.counts = p.counts;
+    ap.offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
+    ap.sorted_ids = p.sorted_ids;
+    ap.tile_expert = p.block_expert;
+    ap.num_padded = p.num_padded;
+    if (launch_align(ap, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  }
   p.h = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
   p.xq = ws + L.xq;
   p.hq = ws + L.hq;

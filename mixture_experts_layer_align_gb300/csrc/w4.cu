@@ -33,6 +33,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "route_token.cuh"
 
 namespace moe {
 namespace {
@@ -42,7 +43,7 @@ constexpr int kStepK = 256;     // columns of a stage
 constexpr int kCodeBytes = kRows * kStepK / 2;  // of a stage
 constexpr int kMaxStages = 6;
 constexpr int kRedTokens = 8, kRedBytes = kRedTokens * kRows * 4;  // sums on their way out
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kSmSmem = 228 * 1024, kMaxSmem = 226 * 1024;  // of an SM; dynamic, of a block
 constexpr int kStaticSmem = 1024 + 256;  // what else a block takes of them
 constexpr int kRowThreads = 128;  // one per row
@@ -183,15 +184,31 @@ __device__ __forceinline__ int x_chunk(int t, int c8) {
   return t * 128 + ((c8 / 2) ^ (t & 7)) * 16 + c8 % 2 * 8;
 }
 
-// x, split, for blocks of more than eight tokens: a warp for 256 columns of a row.
-// Layer: the rows of the pairs in sorted_ids, row pair / k of x.
+// 256 columns of a row, split by a warp to row `at` of the blocks of tokens.
+__device__ __forceinline__ void split_row(const __nv_bfloat16* row, int K, int step, int nt,
+                                          int group, uint8_t* xq, long long at) {
+  const XLayout lay(K, nt, group);
+  const int lane = threadIdx.x % 32, t = static_cast<int>(at % nt), blk = 2 * step + lane / 16,
+            c8 = lane % 16, c = step * 32 + lane;
+  uint8_t* to = xq + at / nt * lay.bytes();
+  const uint4 w = c < K / 8 ? __ldg(reinterpret_cast<const uint4*>(row) + c) : make_uint4(0, 0, 0, 0);
+  float sum, factor;
+  split_columns(w, group / 8, to + static_cast<size_t>(blk) * kPieces * x_piece_bytes(nt) + x_chunk(t, c8),
+                x_piece_bytes(nt), sum, factor);
+  float* side = reinterpret_cast<float*>(to + lay.sides() + static_cast<size_t>(blk) * lay.side) + t;
+  if (c8 % (group / 8) == 0) side[c8 / (group / 8) * nt] = sum;
+  if (c8 == 0) side[kBlockK / group * nt] = factor;
+}
+
+// x, split: a warp for 256 columns of a row.  Layer: the rows of the pairs in
+// sorted_ids, row pair / k of x.
 __global__ void __launch_bounds__(kSplitThreads)
     w4_split_kernel(const __nv_bfloat16* __restrict__ x, int T, int K, int nt, int group,
                     uint8_t* __restrict__ xq, const int32_t* __restrict__ sorted_ids,
                     const int32_t* __restrict__ num_padded, int P, int k) {
   pdl_wait();
   pdl_trigger();
-  const int steps = (K + kStepK - 1) / kStepK, lane = threadIdx.x % 32;
+  const int steps = (K + kStepK - 1) / kStepK;
   const long long item = blockIdx.x * (kSplitThreads / 32ll) + threadIdx.x / 32;
   const long long at = item / steps;
   const int step = static_cast<int>(item - at * steps);
@@ -204,17 +221,90 @@ __global__ void __launch_bounds__(kSplitThreads)
   } else if (at >= T) {
     return;
   }
-  const XLayout lay(K, nt, group);
-  const int t = static_cast<int>(at % nt), blk = 2 * step + lane / 16, c8 = lane % 16;
-  uint8_t* to = xq + at / nt * lay.bytes();
-  const int c = step * 32 + lane;
-  const uint4 w = c < K / 8 ? __ldg(reinterpret_cast<const uint4*>(x + row * K) + c) : make_uint4(0, 0, 0, 0);
-  float sum, factor;
-  split_columns(w, group / 8, to + static_cast<size_t>(blk) * kPieces * x_piece_bytes(nt) + x_chunk(t, c8),
-                x_piece_bytes(nt), sum, factor);
-  float* side = reinterpret_cast<float*>(to + lay.sides() + static_cast<size_t>(blk) * lay.side) + t;
-  if (c8 % (group / 8) == 0) side[c8 / (group / 8) * nt] = sum;
-  if (c8 == 0) side[kBlockK / group * nt] = factor;
+  split_row(x + row * K, K, step, nt, group, xq, at);
+}
+
+// For few pairs, the router, the alignment and the split of x in one kernel: every
+// block routes all tokens and sorts all pairs (a few microseconds, which three kernels
+// in a row spend on starting), then splits its share; the first one writes the lists.
+constexpr int kFrontThreads = 1024, kFrontPairs = 512, kFrontExperts = 256;
+struct W4FrontJob {
+  const float* logits;
+  const __nv_bfloat16* x;
+  int T, H, E, k, renorm, nt, group;
+  int32_t* ids;
+  float* wts;
+  int32_t *counts, *sorted_ids, *block_expert, *num_padded;
+  uint8_t* xq;
+  int* err;
+};
+__global__ void __launch_bounds__(kFrontThreads) w4_front_kernel(const W4FrontJob p) {
+  __shared__ __align__(16) int32_t s_ids[kFrontPairs];
+  __shared__ float s_wts[kFrontPairs];
+  __shared__ int32_t s_at[kFrontPairs];  // a pair's row among the sorted ones
+  __shared__ int s_count[kFrontExperts], s_first[kFrontExperts];
+  __shared__ int s_warp[kFrontExperts / 32];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, P = p.T * p.k;
+  pdl_wait();
+  pdl_trigger();
+  for (int t = warp; t < p.T; t += kFrontThreads / 32)
+    route_token_any(p.logits + static_cast<size_t>(t) * p.E, p.E, p.k, p.renorm, nullptr,
+                    s_ids + t * p.k, s_wts + t * p.k, lane);
+  if (tid < kFrontExperts) s_count[tid] = 0;
+  if (tid >= P && tid < (P + 3) / 4 * 4) s_ids[tid] = -1;
+  __syncthreads();
+  // a pair's place among those of its expert: the earlier ones
+  int e = 0, rank = 0;
+  if (tid < P) {
+    e = s_ids[tid];
+    for (int q = 0; q < tid; q += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(s_ids + q);
+      rank += (v.x == e) + (v.y == e && q + 1 < tid) + (v.z == e && q + 2 < tid) +
+              (v.w == e && q + 3 < tid);
+    }
+    atomicAdd(&s_count[e], 1);
+  }
+  __syncthreads();
+  // blocks of the experts before each
+  int count = 0, blocks = 0, sum = 0;
+  if (tid < kFrontExperts) {
+    count = s_count[tid];
+    blocks = sum = (count + p.nt - 1) / p.nt;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+  }
+  __syncthreads();
+  if (tid < kFrontExperts) {
+    for (int w = 0; w < warp; ++w) sum += s_warp[w];
+    s_first[tid] = sum - blocks;
+  }
+  __syncthreads();
+  if (tid < P) s_at[tid] = s_first[e] * p.nt + rank;
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    if (tid == 0) *p.err = 0;
+    if (tid < P) {
+      p.ids[tid] = e;
+      p.wts[tid] = s_wts[tid];
+      p.sorted_ids[s_at[tid]] = tid;
+    }
+    if (tid < p.E) {
+      p.counts[tid] = count;
+      for (int i = 0; i < blocks; ++i) p.block_expert[s_first[tid] + i] = tid;
+      for (int i = count; i < blocks * p.nt; ++i) p.sorted_ids[s_first[tid] * p.nt + i] = P;
+    }
+    if (tid == kFrontExperts - 1) *p.num_padded = sum * p.nt;
+  }
+  const int steps = (p.H + kStepK - 1) / kStepK;
+  for (int i = blockIdx.x * (kFrontThreads / 32) + warp; i < P * steps;
+       i += gridDim.x * (kFrontThreads / 32)) {
+    const int pair = i / steps;
+    split_row(p.x + static_cast<size_t>(pair / p.k) * p.H, p.H, i % steps, p.nt, p.group, p.xq,
+              s_at[pair]);
+  }
 }
 
 enum W4Mode { kMatvec, kGateUp, kDown };
@@ -241,13 +331,14 @@ struct W4Job {
   const int32_t* num_padded;
   const float* wts;
   int P, k;
+  int lists_new; // the kernel before writes the lists
   int* err;      // status word, or null
 };
 
 template <int PG, int NT>
 struct W4Shape {
   static constexpr int kN = NT < 16 ? 16 : NT;  // MMA N (16 at least with 128 rows)
-  static constexpr int kPerSm = NT <= 16 ? 3 : 2;
+  static constexpr int kPerSm = NT == 8 ? 4 : NT == 16 ? 3 : 2;
   static constexpr int kTmem = NT <= 16 ? 128 : 256;  // columns of tensor memory
   // Columns of a unit, what is multiplied at a time: as many as leave room for
   // two buffers of A and two sets of accumulators (one is read during the next
@@ -309,8 +400,10 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
   const int CS = j.cluster;
   const int rank = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const bool layer = j.mode != kMatvec, gate_up = j.mode == kGateUp;
-  // The kernel before splits x, and waited itself for those before it: the weights and
-  // the lists of the alignment are older than it and are read before pdl_wait().
+  // The kernel before splits x, and waited itself for those before it: the weights, and
+  // the lists where it does not write them, are older than it and are read before
+  // pdl_wait().
+  if (j.lists_new) pdl_wait();
   const int n_blocks = layer ? __ldcg(j.num_padded) / NT : j.n_blocks;
   const int n_jobs = n_blocks * j.row_tiles;
   const int job0 = static_cast<int>(blockIdx.x) / CS, job_step = static_cast<int>(gridDim.x) / CS;
@@ -585,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
           const uint64_t zz = pack2(-z_old[i], -z_old[i]), ss = pack2(s_old[i], s_old[i]);
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
+            if (PG < 4 && NT == 8 && n == 2 && my_valid <= 4) break;
             const float4 xv = *reinterpret_cast<const float4*>(sums_old + i * NT + t0 + n / 2 * 4);
             const uint64_t x2 = n % 2 ? pack2(xv.z, xv.w) : pack2(xv.x, xv.y);
             const uint64_t f2 = n % 2 ? pack2(f[n / 2].z, f[n / 2].w) : pack2(f[n / 2].x, f[n / 2].y);
@@ -841,6 +935,10 @@ int w4_layer_block_rows(int T, int E, int k) {
   return T <= 8 || P <= 4ll * E ? 8 : T <= 16 || P <= 8ll * E ? 16 : 32;
 }
 
+bool w4_front_fits(int T, int E, int k) {
+  return static_cast<long long>(T) * k <= kFrontPairs && E <= kFrontExperts;
+}
+
 size_t w4_split_bytes(long long blocks, int nt, int K, int group) {
   return static_cast<size_t>(blocks) * XLayout(K, nt, group).bytes();
 }
@@ -901,9 +999,22 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   j.P = static_cast<int>(P);
   j.k = p.k;
   j.err = p.err;
-  cudaError_t e = launch_split(p.x, p.T, p.H, j.n_blocks, nt, p.w13.group, p.xq, p.sorted_ids,
-                               p.num_padded, j.P, p.k, st);
+  cudaError_t e = cudaSuccess;
+  if (w4_front_fits(p.T, p.E, p.k)) {
+    W4FrontJob f{p.logits, p.x, p.T, p.H, p.E, p.k, p.renorm, nt, p.w13.group, p.ids, p.wts,
+                 p.counts, p.sorted_ids, p.block_expert, p.num_padded, p.xq, p.err};
+    const long long warps = P * ((p.H + kStepK - 1) / kStepK);
+    constexpr int kWarps = kFrontThreads / 32;
+    e = launch_pdl(w4_front_kernel,
+                   dim3(static_cast<unsigned>(std::min<long long>((warps + kWarps - 1) / kWarps, num_sms))),
+                   dim3(kFrontThreads), 0, st, f);
+  } else {
+    e = launch_split(p.x, p.T, p.H, j.n_blocks, nt, p.w13.group, p.xq, p.sorted_ids, p.num_padded,
+                     j.P, p.k, st);
+  }
+  j.lists_new = w4_front_fits(p.T, p.E, p.k) ? 1 : 0;
   if (e == cudaSuccess) e = launch_job(map13, p.w13.group, j, nt, num_sms, st);
+  j.lists_new = 0;
   if (e == cudaSuccess)
     e = launch_split(p.h, 0, p.I, j.n_blocks, nt, p.w2.group, p.hq, p.sorted_ids, p.num_padded,
                      j.P, 1, st);
