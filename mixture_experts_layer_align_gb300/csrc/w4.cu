@@ -335,10 +335,9 @@ struct W4Job {
   int* err;      // status word, or null
 };
 
-template <int PG, int NT>
+template <int PG, int NT, int PS>
 struct W4Shape {
   static constexpr int kN = NT < 16 ? 16 : NT;  // MMA N (16 at least with 128 rows)
-  static constexpr int kPerSm = NT == 8 ? 4 : NT == 16 ? 3 : 2;
   static constexpr int kTmem = NT <= 16 ? 128 : 256;  // columns of tensor memory
   // Columns of a unit, what is multiplied at a time: as many as leave room for
   // two buffers of A and two sets of accumulators (one is read during the next
@@ -380,13 +379,14 @@ __device__ __noinline__ float w4_row_plain(const W4Job& j, int group, size_t gro
   return sum;
 }
 
-// PG: 32-column pieces of a group (1, 2, 4).  NT: tokens of a block at most.
+// PG: 32-column pieces of a group (1, 2, 4).  NT: tokens of a block at most.  PS:
+// thread blocks of an SM.
 // A cluster (of one block, where there are more jobs than clusters) takes every
 // gridDim.x / j.cluster-th job: a tile of rows for a block of tokens.
-template <int PG, bool ZP, int NT>
-__global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
+template <int PG, bool ZP, int NT, int PS>
+__global__ void __launch_bounds__(kThreads, PS)
     w4_kernel(const __grid_constant__ CUtensorMap map, const W4Job j) {
-  using S = W4Shape<PG, NT>;
+  using S = W4Shape<PG, NT, PS>;
   constexpr int kMmaThreads = kRowThreads + 32;  // at the barriers of A
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kMaxStages];   // a stage's codes and x are there
@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, (W4Shape<PG, NT>::kPerSm))
     for (int i = 0; i < j.stages; ++i) issue_codes();
     pdl_wait();
     pdl_trigger();
+    fence_proxy_async_global();  // x was written by ordinary stores
     for (int i = 0; i < j.stages; ++i) issue_x();
     int slot = 0, phase = 0;
     while (c_job < n_jobs) {
@@ -845,6 +846,13 @@ int choose_cluster(int K, long long tiles, int per_sm, int num_sms) {
   return best;
 }
 
+// Thread blocks of the fullest SM, where each takes what it can.  (Clusters do not fill
+// the SMs evenly: an eighth more.)
+long long blocks_per_sm(long long tiles, int cluster, int num_sms) {
+  const long long blocks = tiles * cluster + (cluster > 1 ? tiles * cluster / 8 : 0);
+  return (blocks + num_sms - 1) / num_sms;
+}
+
 // What a kernel may use, set once for a device.
 cudaError_t allow(const void* kernel, std::atomic<uint64_t>& done) {
   int dev = 0;
@@ -865,23 +873,21 @@ cudaError_t allow(const void* kernel, std::atomic<uint64_t>& done) {
   return e;
 }
 
-template <int PG, bool ZP, int NT>
+template <int PG, bool ZP, int NT, int PS>
 cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaStream_t st) {
-  using S = W4Shape<PG, NT>;
+  using S = W4Shape<PG, NT, PS>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow(reinterpret_cast<const void*>(w4_kernel<PG, ZP, NT>), done);
+  const cudaError_t e = allow(reinterpret_cast<const void*>(w4_kernel<PG, ZP, NT, PS>), done);
   if (e != cudaSuccess) return e;
   W4Job j = job;
   j.whole_stages = j.K % kStepK == 0 && reinterpret_cast<uintptr_t>(j.scales) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(j.zeros) % 8 == 0;
-  const int rows = j.mode == kGateUp ? kRows / 2 : kRows;
-  j.row_tiles = (j.n_rows - 1) / rows + 1;
   const long long tiles = static_cast<long long>(j.row_tiles) * j.n_blocks;
-  j.cluster = choose_cluster(j.K, tiles, S::kPerSm, num_sms);
-  const long long blocks = std::min(tiles * j.cluster, static_cast<long long>(S::kPerSm) * num_sms);
+  const long long blocks = std::min(tiles * j.cluster, static_cast<long long>(PS) * num_sms);
   // As many stages as shared memory holds when the SMs share the blocks evenly.
   const int steps = (j.K + kStepK - 1) / kStepK;
-  const int per_sm = j.cluster > 1 ? S::kPerSm : static_cast<int>((blocks + num_sms - 1) / num_sms);
+  const int per_sm = static_cast<int>(
+      std::min<long long>(PS, blocks_per_sm(tiles, j.cluster, num_sms)));
   j.stages = std::min(kMaxStages, (steps + j.cluster - 1) / j.cluster);
   while (j.stages > 1 && S::smem(j.stages) + kStaticSmem > kSmSmem / per_sm) --j.stages;
   cudaLaunchConfig_t cfg{};
@@ -897,15 +903,25 @@ cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaSt
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = j.cluster > 1 ? 2 : 1;
-  return checked(cudaLaunchKernelEx(&cfg, w4_kernel<PG, ZP, NT>, map, j), "kernel launch");
+  return checked(cudaLaunchKernelEx(&cfg, w4_kernel<PG, ZP, NT, PS>, map, j), "kernel launch");
 }
 
 template <int PG, bool ZP>
-cudaError_t launch_tokens(const CUtensorMap& map, const W4Job& j, int nt, int num_sms,
+cudaError_t launch_tokens(const CUtensorMap& map, const W4Job& job, int nt, int num_sms,
                           cudaStream_t st) {
-  if (nt == 8) return launch<PG, ZP, 8>(map, j, num_sms, st);
-  if (nt == 16) return launch<PG, ZP, 16>(map, j, num_sms, st);
-  return launch<PG, ZP, 32>(map, j, num_sms, st);
+  W4Job j = job;
+  const int rows = j.mode == kGateUp ? kRows / 2 : kRows;
+  j.row_tiles = (j.n_rows - 1) / rows + 1;
+  const long long tiles = static_cast<long long>(j.row_tiles) * j.n_blocks;
+  if (nt == 8) {
+    j.cluster = choose_cluster(j.K, tiles, 4, num_sms);
+    if (blocks_per_sm(tiles, j.cluster, num_sms) <= 3)
+      return launch<PG, ZP, 8, 3>(map, j, num_sms, st);
+    return launch<PG, ZP, 8, 4>(map, j, num_sms, st);
+  }
+  j.cluster = choose_cluster(j.K, tiles, nt == 16 ? 3 : 2, num_sms);
+  if (nt == 16) return launch<PG, ZP, 16, 3>(map, j, num_sms, st);
+  return launch<PG, ZP, 32, 2>(map, j, num_sms, st);
 }
 
 cudaError_t launch_job(const CUtensorMap& map, int group, const W4Job& j, int nt, int num_sms,
