@@ -99,6 +99,8 @@ class MoeW4Args(ctypes.Structure):
 def load():
     """Load libmoe_gb300.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -169,12 +171,17 @@ def _ptr(t):
 def _stream(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        # (current_stream().cuda_stream, without the Stream object: 3 us less of a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _require(t, dtype, name, shape=None):
     import torch
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and t.get_device() == torch.cuda.current_device()
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device.index != torch.cuda.current_device():
@@ -500,16 +507,19 @@ def moe_w4_matvec(x, w: W4Tensor, out=None, out_dtype=None, scratch=None, stream
         raise ValueError(f"out must be bfloat16 or float32 (out_dtype {out_dtype}), got {out.dtype}")
     _require(out, out.dtype, "out", (T, N))
     L = load()
-    if scratch is None:
-        scratch = torch.empty(max(16, L.moe_w4_matvec_scratch_size(T, K)), dtype=torch.uint8,
-                              device=x.device)
-        if stream is not None:
-            scratch.record_stream(stream)
-    else:
+    n = 0
+    if scratch is not None:
         _require(scratch, torch.uint8, "scratch")
-    _check(L.moe_w4_matvec(_ptr(x), T, K, N, ctypes.byref(w._c), _ptr(out),
+        n = scratch.numel()
+    else:
+        n = L.moe_w4_matvec_scratch_size(T, K)
+        if n > 0:
+            scratch = torch.empty(n, dtype=torch.uint8, device=x.device)
+            if stream is not None:
+                scratch.record_stream(stream)
+    _check(L.moe_w4_matvec(x.data_ptr(), T, K, N, w._c, out.data_ptr(),
                            MOE_DT_FP32 if out.dtype == torch.float32 else MOE_DT_BF16,
-                           _ptr(scratch), scratch.numel(), _stream(stream)), "moe_w4_matvec")
+                           scratch.data_ptr() if n else None, n, _stream(stream)), "moe_w4_matvec")
     return out
 
 
@@ -573,8 +583,8 @@ def moe_w4_forward(x, router_logits, w13: W4Tensor, w2: W4Tensor, top_k: int,
                      None if topk_ids_out is None else topk_ids_out.data_ptr(),
                      None if topk_w_out is None else topk_w_out.data_ptr(),
                      None if counts_out is None else counts_out.data_ptr())
-    _check(load().moe_w4_forward(ctypes.byref(args), _ptr(workspace), workspace.numel(),
-                                 _stream(stream)), "moe_w4_forward")
+    _check(load().moe_w4_forward(args, workspace.data_ptr(), workspace.numel(), _stream(stream)),
+           "moe_w4_forward")
     return out
 
 

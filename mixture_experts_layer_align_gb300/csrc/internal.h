@@ -180,6 +180,7 @@ cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int
                              cudaStream_t st);
 // Bytes of `blocks` blocks of nt tokens with K columns, split (16-byte aligned).
 size_t w4_split_bytes(long long blocks, int nt, int K, int group);
+size_t w4_matvec_scratch(int T, int K);
 struct W4LayerParams {
   const __nv_bfloat16* x;
   W4View w13, w2;

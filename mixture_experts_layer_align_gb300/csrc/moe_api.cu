@@ -826,8 +826,7 @@ moe_status_t moe_fused_forward_timed(const moe_fused_args* a, void* workspace,
 
 size_t moe_w4_matvec_scratch_size(int T, int K) {
   if (T < 1 || K < 1 || T >= (1 << 20) || K > (1 << 20)) return 0;
-  const int nt = w4_block_rows(T);
-  return w4_split_bytes((T + nt - 1) / nt, nt, K, 32);  // the most of any group
+  return w4_matvec_scratch(T, K);
 }
 
 moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tensor* w, void* out,
@@ -844,7 +843,8 @@ moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tens
   if (T == 0) return MOE_OK;
   if (!x || !out || !aligned(x, 16) || !aligned(out, out_dtype == MOE_DT_FP32 ? 4 : 2))
     return MOE_ERR_INVALID_ARG;
-  if (!scratch || !aligned(scratch, 16) || scratch_bytes < moe_w4_matvec_scratch_size(T, K))
+  const size_t need = moe_w4_matvec_scratch_size(T, K);
+  if (need > 0 && (!scratch || !aligned(scratch, 16) || scratch_bytes < need))
     return MOE_ERR_WORKSPACE;
   DeviceInfo dev;
   st = check_device(&dev);

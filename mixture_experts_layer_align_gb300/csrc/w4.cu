@@ -191,7 +191,7 @@ __device__ __forceinline__ void split_row(const __nv_bfloat16* row, int K, int s
   const int lane = threadIdx.x % 32, t = static_cast<int>(at % nt), blk = 2 * step + lane / 16,
             c8 = lane % 16, c = step * 32 + lane;
   uint8_t* to = xq + at / nt * lay.bytes();
-  const uint4 w = c < K / 8 ? __ldg(reinterpret_cast<const uint4*>(row) + c) : make_uint4(0, 0, 0, 0);
+  const uint4 w = c < K / 8 ? __ldcg(reinterpret_cast<const uint4*>(row) + c) : make_uint4(0, 0, 0, 0);
   float sum, factor;
   split_columns(w, group / 8, to + static_cast<size_t>(blk) * kPieces * x_piece_bytes(nt) + x_chunk(t, c8),
                 x_piece_bytes(nt), sum, factor);
@@ -380,10 +380,10 @@ __device__ __noinline__ float w4_row_plain(const W4Job& j, int group, size_t gro
 }
 
 // PG: 32-column pieces of a group (1, 2, 4).  NT: tokens of a block at most.  PS:
-// thread blocks of an SM.
+// thread blocks of an SM.  OX: one token, which the copying warp splits itself.
 // A cluster (of one block, where there are more jobs than clusters) takes every
 // gridDim.x / j.cluster-th job: a tile of rows for a block of tokens.
-template <int PG, bool ZP, int NT, int PS>
+template <int PG, bool ZP, int NT, int PS, bool OX>
 __global__ void __launch_bounds__(kThreads, PS)
     w4_kernel(const __grid_constant__ CUtensorMap map, const W4Job j) {
   using S = W4Shape<PG, NT, PS>;
@@ -403,14 +403,14 @@ __global__ void __launch_bounds__(kThreads, PS)
   // The kernel before splits x, and waited itself for those before it: the weights, and
   // the lists where it does not write them, are older than it and are read before
   // pdl_wait().
-  if (j.lists_new) pdl_wait();
+  if (OX || j.lists_new) pdl_wait();
   const int n_blocks = layer ? __ldcg(j.num_padded) / NT : j.n_blocks;
   const int n_jobs = n_blocks * j.row_tiles;
   const int job0 = static_cast<int>(blockIdx.x) / CS, job_step = static_cast<int>(gridDim.x) / CS;
   if (job0 >= n_jobs) return;  // (all of its cluster does)
   if (tid == 0) {
     prefetch_tensormap(&map);
-    for (int i = 0; i < j.stages; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_free[i], 1);
+    for (int i = 0; i < j.stages; ++i) mbar_init(&s_full[i], OX ? 2 : 1), mbar_init(&s_free[i], 1);
     mbar_init(&s_done[0], 1);
     mbar_init(&s_done[1], 1);
     fence_mbarrier_init();
@@ -494,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, PS)
       if (elect_one()) {
         uint64_t* bar = &s_full[c_slot];
         uint8_t* dst = smem + c_slot * S::kStageBytes;
-        mbar_arrive_expect_tx(bar, kCodeBytes + 2 * kPieces * x_rows * 128 + S::kSideBytes);
+        mbar_arrive_expect_tx(bar, OX ? kCodeBytes
+                                      : kCodeBytes + 2 * kPieces * x_rows * 128 + S::kSideBytes);
         const int col = (step0 + c_step) * (kStepK / 2);
         tma_load_2d(dst, &map, bar, col, c_row);
         tma_load_2d(dst + kCodeBytes / 2, &map, bar, col, c_row + (gate_up ? j.n_rows : kRows / 2));
@@ -512,9 +513,30 @@ __global__ void __launch_bounds__(kThreads, PS)
     const XLayout lay(j.K, NT, 32 * PG);
     int x_job = job0, x_step = 0, x_slot = 0, side_slot = 0;
     const uint8_t* xq = j.xq + x_job % n_blocks * lay.bytes();
+    // OX: the 256 columns of x to come, on their way
+    uint4 own = make_uint4(0, 0, 0, 0);
+    auto fetch_own = [&]() {
+      const int c = (step0 + x_step) * (kStepK / 8) + lane;
+      own = c < j.K / 8 ? __ldcg(reinterpret_cast<const uint4*>(j.x) + c) : make_uint4(0, 0, 0, 0);
+    };
+    auto split_own = [&]() {
+      const int blk = lane / 16, c8 = lane % 16;
+      uint8_t* to = smem + x_slot * S::kStageBytes + kCodeBytes + blk * S::kXBytes;
+      float* side = reinterpret_cast<float*>(sides + side_slot * S::kSideBytes) + blk * (4 / PG + 1) * NT;
+      float sum, factor;
+      split_columns(own, 4 * PG, to + x_chunk(0, c8), x_piece_bytes(NT), sum, factor);
+      if (c8 % (4 * PG) == 0) side[c8 / (4 * PG) * NT] = sum;
+      if (c8 == 0) side[4 / PG * NT] = factor;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_full[x_slot]);
+    };
+    if (OX) fetch_own();
     auto issue_x = [&]() {
       if (x_job >= n_jobs) return;
-      if (elect_one()) {
+      if (OX) {
+        split_own();
+      } else if (elect_one()) {
         uint64_t* bar = &s_full[x_slot];
         uint8_t* dst = smem + x_slot * S::kStageBytes + kCodeBytes;
         const size_t step = step0 + x_step;
@@ -536,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, PS)
         x_job += job_step;
         xq = j.xq + x_job % n_blocks * lay.bytes();
       }
+      if (OX && x_job < n_jobs) fetch_own();
     };
     for (int i = 0; i < j.stages; ++i) issue_codes();
     pdl_wait();
@@ -833,6 +856,11 @@ __global__ void __launch_bounds__(256)
 
 // Thread blocks that split K, a cluster: as many as leave the busiest SM the fewest
 // stages, of those that run at once.
+// One token is split where it is used: no kernel before, no scratch.  (2048 x 2048: 5.2
+// against 5.9 us, and a launch of the host's less; 8192 x 57344 the same.  With two tokens
+// the copying warp falls behind, 50 against 46 us there.)
+bool own_x(int T) { return T == 1; }
+
 int choose_cluster(int K, long long tiles, int per_sm, int num_sms) {
   const int steps = (K + kStepK - 1) / kStepK;
   int best = 1;
@@ -873,11 +901,11 @@ cudaError_t allow(const void* kernel, std::atomic<uint64_t>& done) {
   return e;
 }
 
-template <int PG, bool ZP, int NT, int PS>
+template <int PG, bool ZP, int NT, int PS, bool OX = false>
 cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaStream_t st) {
   using S = W4Shape<PG, NT, PS>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow(reinterpret_cast<const void*>(w4_kernel<PG, ZP, NT, PS>), done);
+  const cudaError_t e = allow(reinterpret_cast<const void*>(w4_kernel<PG, ZP, NT, PS, OX>), done);
   if (e != cudaSuccess) return e;
   W4Job j = job;
   j.whole_stages = j.K % kStepK == 0 && reinterpret_cast<uintptr_t>(j.scales) % 16 == 0 &&
@@ -903,7 +931,7 @@ cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaSt
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = j.cluster > 1 ? 2 : 1;
-  return checked(cudaLaunchKernelEx(&cfg, w4_kernel<PG, ZP, NT, PS>, map, j), "kernel launch");
+  return checked(cudaLaunchKernelEx(&cfg, w4_kernel<PG, ZP, NT, PS, OX>, map, j), "kernel launch");
 }
 
 template <int PG, bool ZP>
@@ -915,9 +943,12 @@ cudaError_t launch_tokens(const CUtensorMap& map, const W4Job& job, int nt, int 
   const long long tiles = static_cast<long long>(j.row_tiles) * j.n_blocks;
   if (nt == 8) {
     j.cluster = choose_cluster(j.K, tiles, 4, num_sms);
+    const bool own = j.mode == kMatvec && own_x(j.T);
     if (blocks_per_sm(tiles, j.cluster, num_sms) <= 3)
-      return launch<PG, ZP, 8, 3>(map, j, num_sms, st);
-    return launch<PG, ZP, 8, 4>(map, j, num_sms, st);
+      return own ? launch<PG, ZP, 8, 3, true>(map, j, num_sms, st)
+                 : launch<PG, ZP, 8, 3>(map, j, num_sms, st);
+    return own ? launch<PG, ZP, 8, 4, true>(map, j, num_sms, st)
+               : launch<PG, ZP, 8, 4>(map, j, num_sms, st);
   }
   j.cluster = choose_cluster(j.K, tiles, nt == 16 ? 3 : 2, num_sms);
   if (nt == 16) return launch<PG, ZP, 16, 3>(map, j, num_sms, st);
@@ -955,6 +986,11 @@ bool w4_front_fits(int T, int E, int k) {
   return static_cast<long long>(T) * k <= kFrontPairs && E <= kFrontExperts;
 }
 
+size_t w4_matvec_scratch(int T, int K) {
+  const int nt = w4_block_rows(T);
+  return own_x(T) ? 0 : w4_split_bytes((T + nt - 1) / nt, nt, K, 32);  // the most of any group
+}
+
 size_t w4_split_bytes(long long blocks, int nt, int K, int group) {
   return static_cast<size_t>(blocks) * XLayout(K, nt, group).bytes();
 }
@@ -988,6 +1024,7 @@ cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int
   j.T = T;
   j.out = out;
   j.out_fp32 = out_fp32 ? 1 : 0;
+  if (own_x(T)) return launch_job(map, w.group, j, nt, num_sms, st);
   const cudaError_t e =
       launch_split(x, T, K, j.n_blocks, nt, w.group, scratch, nullptr, nullptr, 0, 1, st);
   if (e != cudaSuccess) return e;
