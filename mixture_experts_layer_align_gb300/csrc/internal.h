@@ -195,7 +195,7 @@ struct W4LayerParams {
   int32_t* sorted_ids;          // pair ids by expert in blocks of w4_layer_block_rows(), T*k pads
   int32_t* block_expert;        // expert of each block
   int32_t* num_padded;          // rows of all blocks
-  __nv_bfloat16* h;             // [T*k][I]
+  float* h;                     // [T*k][I]
   uint8_t *xq, *hq;             // x and h of the blocks, split
   float* y;                     // [T*k][H]
   __nv_bfloat16* out;

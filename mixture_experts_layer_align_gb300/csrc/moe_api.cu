@@ -757,7 +757,7 @@ W4Layout make_w4_layout(int T, int H, int I, int E, int k) {
   L.sorted = take(sizeof(int32_t) * rows);
   L.blocks = take(sizeof(int32_t) * (rows / bm));
   L.padded = take(sizeof(int32_t));
-  L.h = take(sizeof(__nv_bfloat16) * P * I);
+  L.h = take(sizeof(float) * P * I);
   const long long pairs = static_cast<long long>(P);
   const long long blocks =
       std::min(pairs, (pairs + std::min<long long>(E, pairs) * (bm - 1)) / bm);
@@ -925,7 +925,7 @@ moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t worksp
     ap.num_padded = p.num_padded;
     if (launch_align(ap, stream) != cudaSuccess) return MOE_ERR_CUDA;
   }
-  p.h = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
+  p.h = reinterpret_cast<float*>(ws + L.h);
   p.xq = ws + L.xq;
   p.hq = ws + L.hq;
   p.y = reinterpret_cast<float*>(ws + L.y);

@@ -116,6 +116,12 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// Two fp16 numbers to E5M2, to nearest; the low byte is the low half's.
+__device__ __forceinline__ uint32_t cvt_e5m2x2(uint32_t a) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -139,40 +145,74 @@ __device__ constexpr uint32_t w4_idesc(int N) {
   return (1u << 4) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// 256 columns of a token, split by a warp: w holds the lane's eight.  The pieces of
+// Eight columns of a row, bf16 (x) or fp32 (h), zeros past its end.
+template <typename T>
+struct Columns {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* row, int c, int K) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + c * 8);
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 v = c * 8 < K ? __ldcg(p + i) : make_uint4(0, 0, 0, 0);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+  // largest magnitude, as fp32 bits (as integers they order like the numbers, infinity
+  // and NaN above all)
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (kWords == 4) {
+      const uint32_t m = max_bf16x2(max_bf16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                    max_bf16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+      return max(m & 0xffffu, m >> 16) << 16;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
+    }
+  }
+  __device__ __forceinline__ uint64_t pair(int n) const {  // columns 2n and 2n + 1
+    if constexpr (kWords == 4) return pack2(bf16_lo(w[n]), bf16_hi(w[n]));
+    else return pack2(__uint_as_float(w[2 * n]), __uint_as_float(w[2 * n + 1]));
+  }
+};
+
+// 256 columns of a token, split by a warp: v holds the lane's eight.  The pieces of
 // the eight columns go to `to` + n * piece_bytes; `sum` is that of the lane's group,
 // in every lane of it.  Columns with an infinity or NaN get the factor NaN: the sums
 // that they enter are formed again from x itself.
-__device__ __forceinline__ void split_columns(uint4 w, int group_lanes, uint8_t* to,
+template <typename T>
+__device__ __forceinline__ void split_columns(const Columns<T>& v, int group_lanes, uint8_t* to,
                                               int piece_bytes, float& sum, float& factor) {
-  uint32_t m = max_bf16x2(max_bf16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                          max_bf16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-  // (magnitudes as integers order like the numbers, infinity and NaN above all)
-  const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) << 16;
+  const uint32_t top = __reduce_max_sync(0xffffffffu, v.top());
   const bool finite = top < 0x7f800000u;
   // biased exponent of the largest; at least 14, so that the scale stays finite
   const int ex = max(finite ? static_cast<int>(top >> 23) : 0, 14);
   const float scale = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(141 - ex)
   factor = finite ? __uint_as_float(static_cast<uint32_t>(ex - 5) << 23) : __int_as_float(0x7fc00000);
   const uint64_t scale2 = pack2(scale, scale);
-  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
   uint64_t s2 = 0;
   uint32_t h[4];
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    const uint64_t v = finite ? mul2(pack2(bf16_lo(ww[n]), bf16_hi(ww[n])), scale2) : 0;
+    const uint64_t x2 = finite ? mul2(v.pair(n), scale2) : 0;
     float lo, hi;
-    unpack2(v, lo, hi);
-    s2 = n == 0 ? v : add2(s2, v);
+    unpack2(x2, lo, hi);
+    s2 = n == 0 ? x2 : add2(s2, x2);
     h[n] = cvt_f16x2(lo, hi);
   }
 #pragma unroll
   for (int n = 0; n < kPieces; ++n) {
-    const uint32_t a = __byte_perm(h[0], h[1], 0x7351), b = __byte_perm(h[2], h[3], 0x7351);
+    uint32_t c[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      c[q] = cvt_e5m2x2(h[q]);
+      h[q] = sub_f16x2(h[q], __byte_perm(c[q], 0, 0x1404));  // (a piece is the top byte of its fp16)
+    }
+    const uint32_t a = __byte_perm(c[0], c[1], 0x5140), b = __byte_perm(c[2], c[3], 0x5140);
     *reinterpret_cast<uint2*>(to + n * piece_bytes) =
         make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-#pragma unroll
-    for (int q = 0; q < 4; ++q) h[q] = sub_f16x2(h[q], h[q] & 0xff00ff00u);
   }
   float lo, hi;
   unpack2(s2, lo, hi);
@@ -185,15 +225,17 @@ __device__ __forceinline__ int x_chunk(int t, int c8) {
 }
 
 // 256 columns of a row, split by a warp to row `at` of the blocks of tokens.
-__device__ __forceinline__ void split_row(const __nv_bfloat16* row, int K, int step, int nt,
+template <typename T>
+__device__ __forceinline__ void split_row(const T* row, int K, int step, int nt,
                                           int group, uint8_t* xq, long long at) {
   const XLayout lay(K, nt, group);
   const int lane = threadIdx.x % 32, t = static_cast<int>(at % nt), blk = 2 * step + lane / 16,
             c8 = lane % 16, c = step * 32 + lane;
   uint8_t* to = xq + at / nt * lay.bytes();
-  const uint4 w = c < K / 8 ? __ldcg(reinterpret_cast<const uint4*>(row) + c) : make_uint4(0, 0, 0, 0);
+  Columns<T> v;
+  v.load(row, c, K);
   float sum, factor;
-  split_columns(w, group / 8, to + static_cast<size_t>(blk) * kPieces * x_piece_bytes(nt) + x_chunk(t, c8),
+  split_columns(v, group / 8, to + static_cast<size_t>(blk) * kPieces * x_piece_bytes(nt) + x_chunk(t, c8),
                 x_piece_bytes(nt), sum, factor);
   float* side = reinterpret_cast<float*>(to + lay.sides() + static_cast<size_t>(blk) * lay.side) + t;
   if (c8 % (group / 8) == 0) side[c8 / (group / 8) * nt] = sum;
@@ -202,8 +244,9 @@ __device__ __forceinline__ void split_row(const __nv_bfloat16* row, int K, int s
 
 // x, split: a warp for 256 columns of a row.  Layer: the rows of the pairs in
 // sorted_ids, row pair / k of x.
+template <typename V>
 __global__ void __launch_bounds__(kSplitThreads)
-    w4_split_kernel(const __nv_bfloat16* __restrict__ x, int T, int K, int nt, int group,
+    w4_split_kernel(const V* __restrict__ x, int T, int K, int nt, int group,
                     uint8_t* __restrict__ xq, const int32_t* __restrict__ sorted_ids,
                     const int32_t* __restrict__ num_padded, int P, int k) {
   pdl_wait();
@@ -319,7 +362,7 @@ struct W4Job {
   int row_tiles; // tiles of them, kRows a thread block's (kRows / 2, gate/up)
   int n_blocks;  // blocks of tokens (an upper bound for the layer)
   const uint8_t* xq;        // x (down: h), split: an XLayout for each block of tokens
-  const __nv_bfloat16* x;   // tokens (down: h by pair)
+  const void* x;            // tokens, bf16 (down: h by pair, fp32)
   int T;
   void* out;     // matvec: [T][N]; gate/up: h bf16 [pair][I]; down: y fp32 [pair][H]
   int out_fp32;
@@ -360,7 +403,7 @@ struct W4Shape {
 // sum_k x[k] (code[k] - zero) * scale over columns k0 .. k1 of a weight row,
 // column by column: what a token with infinities or NaN gets.
 __device__ __noinline__ float w4_row_plain(const W4Job& j, int group, size_t grow,
-                                           const __nv_bfloat16* x, int k0, int k1) {
+                                           size_t x_row, int k0, int k1) {
   const size_t g0 = grow * ((j.K + group - 1) / group);
   float sum = 0.f;
   for (int k = k0; k < k1;) {
@@ -372,7 +415,10 @@ __device__ __noinline__ float w4_row_plain(const W4Job& j, int group, size_t gro
     float part = 0.f;
     for (; k < end; ++k) {
       const int code = j.codes[grow * (j.K / 2) + k / 2] >> (k % 2 * 4) & 15;
-      part = fmaf(__bfloat162float(x[k]), static_cast<float>(code) - zero, part);
+      const size_t at = x_row * j.K + k;
+      const float x = j.mode == kDown ? static_cast<const float*>(j.x)[at]
+                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(j.x)[at]);
+      part = fmaf(x, static_cast<float>(code) - zero, part);
     }
     sum = fmaf(scale, part, sum);
   }
@@ -514,10 +560,9 @@ __global__ void __launch_bounds__(kThreads, PS)
     int x_job = job0, x_step = 0, x_slot = 0, side_slot = 0;
     const uint8_t* xq = j.xq + x_job % n_blocks * lay.bytes();
     // OX: the 256 columns of x to come, on their way
-    uint4 own = make_uint4(0, 0, 0, 0);
+    Columns<__nv_bfloat16> own;
     auto fetch_own = [&]() {
-      const int c = (step0 + x_step) * (kStepK / 8) + lane;
-      own = c < j.K / 8 ? __ldcg(reinterpret_cast<const uint4*>(j.x) + c) : make_uint4(0, 0, 0, 0);
+      own.load(static_cast<const __nv_bfloat16*>(j.x), (step0 + x_step) * (kStepK / 8) + lane, j.K);
     };
     auto split_own = [&]() {
       const int blk = lane / 16, c8 = lane % 16;
@@ -642,19 +687,19 @@ __global__ void __launch_bounds__(kThreads, PS)
       if (j.whole_stages) {
         if (j.scale_bf16) {
           const uint8_t* p = static_cast<const uint8_t*>(j.scales) + at * 2;
-          if (PG == 4) s_raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-          if (PG == 2) load_raw(s_raw, reinterpret_cast<const uint2*>(p));
-          if (PG == 1) load_raw(s_raw, reinterpret_cast<const uint4*>(p));
+          if constexpr (PG == 4) s_raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          if constexpr (PG == 2) load_raw(s_raw, reinterpret_cast<const uint2*>(p));
+          if constexpr (PG == 1) load_raw(s_raw, reinterpret_cast<const uint4*>(p));
         } else {
           const uint8_t* p = static_cast<const uint8_t*>(j.scales) + at * 4;
-          if (PG == 4) load_raw(s_raw, reinterpret_cast<const uint2*>(p));
-          if (PG <= 2) load_raw(s_raw, reinterpret_cast<const uint4*>(p));
-          if (PG == 1) load_raw(s_raw + 4, reinterpret_cast<const uint4*>(p) + 1);
+          if constexpr (PG == 4) load_raw(s_raw, reinterpret_cast<const uint2*>(p));
+          if constexpr (PG <= 2) load_raw(s_raw, reinterpret_cast<const uint4*>(p));
+          if constexpr (PG == 1) load_raw(s_raw + 4, reinterpret_cast<const uint4*>(p) + 1);
         }
         if (ZP) {
-          if (PG == 4) z_raw[0] = __ldg(reinterpret_cast<const uint16_t*>(j.zeros + at));
-          if (PG == 2) z_raw[0] = __ldg(reinterpret_cast<const uint32_t*>(j.zeros + at));
-          if (PG == 1) load_raw(z_raw, reinterpret_cast<const uint2*>(j.zeros + at));
+          if constexpr (PG == 4) z_raw[0] = __ldg(reinterpret_cast<const uint16_t*>(j.zeros + at));
+          if constexpr (PG == 2) z_raw[0] = __ldg(reinterpret_cast<const uint32_t*>(j.zeros + at));
+          if constexpr (PG == 1) load_raw(z_raw, reinterpret_cast<const uint2*>(j.zeros + at));
         }
         return;
       }
@@ -808,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, PS)
             if (isnan(red[t * kRows + tid]))
               red[t * kRows + tid] =
                   w4_row_plain(j, 32 * PG, this_row,
-                               j.x + static_cast<size_t>(gate_up ? pair / j.k : pair) * j.K, k0, k1);
+                               static_cast<size_t>(gate_up ? pair / j.k : pair), k0, k1);
           }
         }
         if (CS > 1) continue;
@@ -997,13 +1042,14 @@ size_t w4_split_bytes(long long blocks, int nt, int K, int group) {
 
 namespace {
 
-cudaError_t launch_split(const __nv_bfloat16* x, int T, int K, int n_blocks, int nt, int group,
+template <typename V>
+cudaError_t launch_split(const V* x, int T, int K, int n_blocks, int nt, int group,
                          uint8_t* xq, const int32_t* sorted_ids, const int32_t* num_padded, int P,
                          int k, cudaStream_t st) {
 
   const long long warps = static_cast<long long>(n_blocks) * nt * ((K + kStepK - 1) / kStepK);
   constexpr int kWarps = kSplitThreads / 32;
-  return launch_pdl(w4_split_kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)),
+  return launch_pdl(w4_split_kernel<V>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)),
                     dim3(kSplitThreads), 0, st, x, T, K, nt, group, xq, sorted_ids, num_padded, P, k);
 }
 
@@ -1038,6 +1084,7 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   W4Job j{};
   set_weight(j, p.w13);
   j.mode = kGateUp;
+  j.out_fp32 = 1;
   j.K = p.H;
   j.n_rows = p.I;
   j.n_blocks = static_cast<int>(std::min(P, (P + std::min<long long>(p.E, P) * (nt - 1)) / nt));
@@ -1074,7 +1121,6 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   if (e != cudaSuccess) return e;
   set_weight(j, p.w2);
   j.mode = kDown;
-  j.out_fp32 = 1;
   j.K = p.I;
   j.n_rows = p.H;
   j.xq = p.hq;
