@@ -4,25 +4,35 @@
 //   y[t][r] = sum over groups of scale[r][g] * sum_k x[t][k] (code[r][k] - zero[r][g])
 //           = sum over groups of scale[r][g] * (D[r][g][t] - zero[r][g] X[g][t]),
 //   D = sum_k code x, X = sum_k x.
-// At a few tokens the codes' bytes bound it, if turning them into an MMA operand
-// does not: at 6.8 TB/s an SM takes in 47 codes a clock.  So they are hardly
-// turned at all.  A byte 0..15 read as E4M3 is that many times 2^-9 (the two lowest
-// exponents share their spacing): the nibbles of a word, spread over bytes by two
-// masks and a shift, are the A operand of tcgen05.mma kind::f8f6f4.  x becomes three
-// E5M2 pieces whose sum it is, one MMA each into the same accumulator:
-// a power of two brings the largest |x| of a token to 2^14 .. 2^15, where x is
-// an fp16 value of 8 significant bits; a piece is the top byte of what is left (a
-// sign, 5 exponent and 2 mantissa bits: E5M2, three significant bits), so the third
-// leaves nothing but what lies 2^-31 below the largest.  Products are exact and
-// sums are fp32 (the MMA was checked to keep addends 2^-23 below the sum).
 //
-// x, and h, is split once for a call, by a kernel of its own, into the image that
-// shared memory needs.  A thread block owns 128
-// weight rows and a slice of K; the blocks of a cluster share rows and split K.  TMA
-// brings 256 columns of the codes (128 bytes of a row) a stage, and x block by block
-// of 128 columns.  Four warps, a thread per row, spread the codes of a unit into
-// tensor memory (A, 128 rows) and, while its MMAs run, scale the sums of the unit
-// before, again a thread per row, in fp32; a fifth warp issues the copies and MMAs.
+// Bound: the codes' bytes, if turning them into an operand does not cost more: at
+// 6.8 TB/s an SM takes in 47 codes a clock.  So they are hardly turned at all.  A byte
+// 0..15 read as E4M3 is that many times 2^-9 (the two lowest exponents share their
+// spacing): the nibbles of a word, spread over bytes by two masks and a shift, are the A
+// operand of tcgen05.mma kind::f8f6f4.  x becomes three E5M2 pieces whose sum it is, one
+// MMA each into the same accumulator: a power of two for each token and 256 columns
+// brings their largest |x| to 2^14 .. 2^15, where x is an fp16 number; a piece is what is
+// left, rounded to E5M2 (three significant bits, to nearest, so each piece leaves an
+// eighth at most of its last), and three leave nothing of a bf16 x but what lies 2^-31
+// below the largest, and 2^-11 of an fp32 h.  Products are exact and sums are fp32 (the
+// MMA was checked to keep addends 2^-23 below the sum).
+// (mma.sync from registers, a bf16 multiply-add for each pair of codes, took 24 us for a
+// token at 4096 x 28672, this 16; bf16 codes in tensor memory twice the stores.)
+//
+// x is split once for a call, by a kernel before, for a single token by the kernel that
+// uses it.  A thread block owns 128 weight rows for a block of 8, 16 or 32 tokens at a
+// time; it stays for all its jobs, so that copies run on from one to the next (a block
+// for each job, most of them empty for a layer's upper bound of them: 185 against 120 us,
+// gate/up of 32 tokens on 256 experts).  Where there are fewer jobs than blocks that run
+// at once, a cluster splits K.  One warp copies, as many stages of 256 columns ahead as
+// fit (codes by TMA, 128 bytes of a row, and x with them: with x half as deep as the
+// codes 8192 x 57344 took 52 us, not 44); one issues MMAs; four, a thread per row, spread
+// the codes of a unit into tensor memory (A, 128 rows) and, while its MMAs run, scale the
+// sums of the unit before in fp32.
+//
+// Measured (device, one call of many in a row): one token at 8192 x 57344 44 us, 80 % of
+// the bytes' time; at 4096 x 28672 16; 2048 x 2048 5.1.  32 tokens at 8192 x 57344 75,
+// where adding up the sums takes as long as the codes.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -61,7 +71,7 @@ __host__ __device__ constexpr int x_piece_bytes(int nt) { return nt * kBlockK; }
 __host__ __device__ constexpr int x_side_bytes(int nt, int group) {
   return (kBlockK / group + 1) * nt * 4;
 }
-// Where they lie for all of K: the pieces of every block, then the rest of every block.
+// Where they lie for all of K (whole stages): the pieces of every block, then the rest.
 struct XLayout {
   int n_cols, nt, side;
   __host__ __device__ XLayout(int K, int nt_, int group)
@@ -270,7 +280,9 @@ __global__ void __launch_bounds__(kSplitThreads)
 // For few pairs, the router, the alignment and the split of x in one kernel: every
 // block routes all tokens and sorts all pairs (a few microseconds, which three kernels
 // in a row spend on starting), then splits its share; the first one writes the lists.
-constexpr int kFrontThreads = 1024, kFrontPairs = 512, kFrontExperts = 256;
+// (One token on 128 experts 22.0 against 23.7 us, 16 tokens 60 against 64, 256 pairs on
+// 256 experts 176 against 181, but 512 pairs on 128 experts 85 against 83.)
+constexpr int kFrontThreads = 1024, kFrontPairs = 256, kFrontExperts = 256;
 struct W4FrontJob {
   const float* logits;
   const __nv_bfloat16* x;
@@ -899,13 +911,15 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Thread blocks that split K, a cluster: as many as leave the busiest SM the fewest
-// stages, of those that run at once.
 // One token is split where it is used: no kernel before, no scratch.  (2048 x 2048: 5.2
 // against 5.9 us, and a launch of the host's less; 8192 x 57344 the same.  With two tokens
 // the copying warp falls behind, 50 against 46 us there.)
 bool own_x(int T) { return T == 1; }
 
+// Thread blocks that split K, a cluster: of the powers of two that run at once, the one
+// that leaves the busiest SM the fewest stages, the largest of equal ones.  (Up to 16, not
+// 8: 1027 rows of 7200 columns 7.4 against 8.1 us.  Any number, not powers of two: 14336 x
+// 4096 with 14 blocks 20.2 against 17.1 us.  The smallest of equal ones: 64 tokens at 7168 x 4096 36 against 26 us.)
 int choose_cluster(int K, long long tiles, int per_sm, int num_sms) {
   const int steps = (K + kStepK - 1) / kStepK;
   int best = 1;
@@ -986,6 +1000,9 @@ cudaError_t launch_tokens(const CUtensorMap& map, const W4Job& job, int nt, int 
   const int rows = j.mode == kGateUp ? kRows / 2 : kRows;
   j.row_tiles = (j.n_rows - 1) / rows + 1;
   const long long tiles = static_cast<long long>(j.row_tiles) * j.n_blocks;
+  // Up to eight tokens: four blocks an SM, or three, with more registers and a stage more,
+  // where those hold all jobs.  (8192 x 57344, 448 jobs: 44.5 against 45.3 us; 4096 x 28672
+  // in pairs, 448 blocks that need not fit three an SM: 16.8 against 16.0.)
   if (nt == 8) {
     j.cluster = choose_cluster(j.K, tiles, 4, num_sms);
     const bool own = j.mode == kMatvec && own_x(j.T);
@@ -1020,11 +1037,18 @@ void set_weight(W4Job& j, const W4View& w) {
 
 }  // namespace
 
+// The smallest block that takes all tokens, else 32.  (8192 x 28672, us with blocks of 8,
+// 16, 32: 12 tokens 40, 31, 37; 20 tokens 62, 45, 39; 48 tokens 103, 72, 73.)
 int w4_block_rows(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : 32; }
 
+// Layer: the block holds the mean of an expert's pairs with a third to spare.  (128
+// experts of 2048 x 768, us with blocks of 8, 16, 32: 4 pairs an expert 85, 91, 107; 6: 91,
+// 94, 117; 8: 112, 99, 123; 12: -, 109, 134; 8 experts of 4096 x 14336, 16 pairs each: -,
+// 214, 199.  Skewed routing would like larger ones: 32 tokens on 256 experts 176, 155,
+// 168; it is not known when the call is enqueued.)
 int w4_layer_block_rows(int T, int E, int k) {
   const long long P = static_cast<long long>(T) * k;
-  return T <= 8 || P <= 4ll * E ? 8 : T <= 16 || P <= 8ll * E ? 16 : 32;
+  return T <= 8 || P <= 6ll * E ? 8 : T <= 16 || P <= 12ll * E ? 16 : 32;
 }
 
 bool w4_front_fits(int T, int E, int k) {
