@@ -462,9 +462,11 @@ __global__ void __launch_bounds__(kThreads, PS)
   // the lists where it does not write them, are older than it and are read before
   // pdl_wait().
   if (OX || j.lists_new) pdl_wait();
+  const int job0 = static_cast<int>(blockIdx.x) / CS, job_step = static_cast<int>(gridDim.x) / CS;
+  // (the first job's expert with the number of jobs; it is one's number if there is one)
+  const int expert0 = layer ? __ldcg(j.block_expert + job0 / j.row_tiles) : 0;
   const int n_blocks = layer ? __ldcg(j.num_padded) / NT : j.n_blocks;
   const int n_jobs = n_blocks * j.row_tiles;
-  const int job0 = static_cast<int>(blockIdx.x) / CS, job_step = static_cast<int>(gridDim.x) / CS;
   if (job0 >= n_jobs) return;  // (all of its cluster does)
   if (tid == 0) {
     prefetch_tensormap(&map);
@@ -483,13 +485,13 @@ __global__ void __launch_bounds__(kThreads, PS)
 
   // a job's rows of the result, and the expert (layer) that they are of
   const int rows_out = gate_up ? kRows / 2 : kRows;
-  auto job_row = [&](int job) { return job / n_blocks * rows_out; };
+  auto job_row = [&](int job) { return job % j.row_tiles * rows_out; };
   auto job_expert = [&](int job) {
-    return layer && job < n_jobs ? __ldcg(j.block_expert + job % n_blocks) : 0;
+    return layer && job < n_jobs ? __ldcg(j.block_expert + job / j.row_tiles) : 0;
   };
   // lane t: token t's pair (matvec: token), and how many there are
   auto job_pair = [&](int job) {
-    const int at = job % n_blocks * NT + lane;
+    const int at = job / j.row_tiles * NT + lane;
     if (!layer) return at;
     return lane < NT && job < n_jobs ? __ldcg(j.sorted_ids + at) : j.P;
   };
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, PS)
     // The next stage, of this job or one to come: its codes, and what comes after
     // pdl_wait(), its x.
     int c_job = job0, c_step = 0, c_slot = 0, c_count = 0, c_row, c_next_expert;
-    c_row = job_expert(c_job) * expert_rows + job_row(c_job);
+    c_row = expert0 * expert_rows + job_row(c_job);
     c_next_expert = job_expert(c_job + job_step);
     const int x_rows = layer ? NT : min(NT, (j.T + 7) / 8 * 8);
     auto issue_codes = [&]() {
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, PS)
     };
     const XLayout lay(j.K, NT, 32 * PG);
     int x_job = job0, x_step = 0, x_slot = 0, side_slot = 0;
-    const uint8_t* xq = j.xq + x_job % n_blocks * lay.bytes();
+    const uint8_t* xq = j.xq + x_job / j.row_tiles * lay.bytes();
     // OX: the 256 columns of x to come, on their way
     Columns<__nv_bfloat16> own;
     auto fetch_own = [&]() {
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, PS)
       if (++x_step == n_steps) {
         x_step = 0;
         x_job += job_step;
-        xq = j.xq + x_job % n_blocks * lay.bytes();
+        xq = j.xq + x_job / j.row_tiles * lay.bytes();
       }
       if (OX && x_job < n_jobs) fetch_own();
     };
@@ -675,9 +677,9 @@ __global__ void __launch_bounds__(kThreads, PS)
     const int groups = (j.K + 32 * PG - 1) / (32 * PG);
     constexpr int kGroups = 8 / PG, kBlkGroups = 4 / PG;
     size_t grow, group0;  // this thread's weight row, and its first group in this slice of K
-    auto find_row = [&](int job) {
+    auto find_row = [&](int job, int expert) {
       const int r0 = job_row(job);  // past the result's last row: that one
-      grow = static_cast<size_t>(job_expert(job)) * expert_rows + min(r0 + tid % rows_out, j.n_rows - 1) +
+      grow = static_cast<size_t>(expert) * expert_rows + min(r0 + tid % rows_out, j.n_rows - 1) +
              (tid >= rows_out ? j.n_rows : 0);
       group0 = grow * groups + k0 / (32 * PG);
       // its scales and zero points on their way to L2
@@ -732,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, PS)
     };
 #pragma unroll
     for (int i = 0; i < (kGroups + 3) / 4; ++i) z_raw[i] = 0;
-    find_row(job0);
+    find_row(job0, expert0);
     fetch_scales(0);
     float s_step[kGroups], s_old[S::kSub], z_old[S::kSub];
     uint32_t z_step[(kGroups + 3) / 4];
@@ -832,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, PS)
         if (step + 1 < n_steps) {
           fetch_scales(step + 1);
         } else if (job + job_step < n_jobs) {
-          find_row(job + job_step);
+          find_row(job + job_step, job_expert(job + job_step));
           fetch_scales(0);
         }
         ok = ok && warp_wait(&s_full[slot], phase);
