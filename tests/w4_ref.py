@@ -34,9 +34,9 @@ def matvec(x, v):
 
 
 def sum_bound(K):
-    """Relative to the sum of the magnitudes: a product passes at most 8 MMA steps of a
-    group, the K/128 group sums of a row and 56 more additions that join warps and
-    thread blocks, each off by at most 2^-23 of what it has summed."""
+    """Relative to the sum of the magnitudes: a product passes at most 12 MMA steps of a
+    group, the K/128 group sums of a row and 52 more operations that scale and join
+    sums, each off by at most 2^-23 of what it has summed."""
     return (K / 128 + 64) * 2.0 ** -23
 
 
