@@ -460,7 +460,7 @@ class W4Tensor:
     and kept; calls use them in place, so they are not to be resized or moved.
     """
 
-    __slots__ = ("codes", "scales", "zeros", "group", "shape", "device", "_c")
+    __slots__ = ("codes", "scales", "zeros", "group", "shape", "device", "_c", "_scratch")
 
     def __init__(self, codes, scales, zeros=None, group: int = 128):
         import torch
@@ -480,9 +480,27 @@ class W4Tensor:
         self.codes, self.scales, self.zeros, self.group = codes, scales, zeros, group
         self.shape = tuple(codes.shape[:-1]) + (K,)
         self.device = codes.device
+        self._scratch = {}
         self._c = MoeW4Tensor(codes.data_ptr(), scales.data_ptr(),
                               None if zeros is None else zeros.data_ptr(),
                               MOE_DT_FP32 if scales.dtype == torch.float32 else MOE_DT_BF16, group)
+
+
+    def _scratch_for(self, n, raw, stream):
+        """n bytes that no call in flight on another stream uses.  A weight keeps one
+        buffer for each current stream it was used on, whose calls follow one another
+        (an allocation is a third of a small call); a call on a `stream` that is not the
+        current one, or under graph capture, gets its own."""
+        import torch
+        if stream is None and not torch.cuda.is_current_stream_capturing():
+            kept = self._scratch.get(raw)
+            if kept is None or kept.numel() < n:
+                kept = self._scratch[raw] = torch.empty(n, dtype=torch.uint8, device=self.device)
+            return kept
+        own = torch.empty(n, dtype=torch.uint8, device=self.device)
+        if stream is not None:
+            own.record_stream(stream)
+        return own
 
 
 def moe_w4_matvec_scratch_size(T: int, K: int) -> int:
@@ -507,19 +525,17 @@ def moe_w4_matvec(x, w: W4Tensor, out=None, out_dtype=None, scratch=None, stream
         raise ValueError(f"out must be bfloat16 or float32 (out_dtype {out_dtype}), got {out.dtype}")
     _require(out, out.dtype, "out", (T, N))
     L = load()
-    n = 0
+    raw = _stream(stream)
     if scratch is not None:
         _require(scratch, torch.uint8, "scratch")
         n = scratch.numel()
     else:
         n = L.moe_w4_matvec_scratch_size(T, K)
         if n > 0:
-            scratch = torch.empty(n, dtype=torch.uint8, device=x.device)
-            if stream is not None:
-                scratch.record_stream(stream)
+            scratch = w._scratch_for(n, raw, stream)
     _check(L.moe_w4_matvec(x.data_ptr(), T, K, N, w._c, out.data_ptr(),
                            MOE_DT_FP32 if out.dtype == torch.float32 else MOE_DT_BF16,
-                           scratch.data_ptr() if n else None, n, _stream(stream)), "moe_w4_matvec")
+                           scratch.data_ptr() if n else None, n, raw), "moe_w4_matvec")
     return out
 
 

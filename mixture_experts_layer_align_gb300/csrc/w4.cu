@@ -438,7 +438,7 @@ __device__ __noinline__ float w4_row_plain(const W4Job& j, int group, size_t gro
 }
 
 // PG: 32-column pieces of a group (1, 2, 4).  NT: tokens of a block at most.  PS:
-// thread blocks of an SM.  OX: one token, which the copying warp splits itself.
+// thread blocks of an SM.  OX: eight tokens at most, which the copying warp splits itself.
 // A cluster (of one block, where there are more jobs than clusters) takes every
 // gridDim.x / j.cluster-th job: a tile of rows for a block of tokens.
 template <int PG, bool ZP, int NT, int PS, bool OX>
@@ -573,19 +573,28 @@ __global__ void __launch_bounds__(kThreads, PS)
     const XLayout lay(j.K, NT, 32 * PG);
     int x_job = job0, x_step = 0, x_slot = 0, side_slot = 0;
     const uint8_t* xq = j.xq + x_job / j.row_tiles * lay.bytes();
-    // OX: the 256 columns of x to come, on their way
-    Columns<__nv_bfloat16> own;
+    // OX: the 256 columns to come of each token, on their way
+    Columns<__nv_bfloat16> own[OX ? NT : 1];
     auto fetch_own = [&]() {
-      own.load(static_cast<const __nv_bfloat16*>(j.x), (step0 + x_step) * (kStepK / 8) + lane, j.K);
+#pragma unroll
+      for (int t = 0; t < (OX ? NT : 1); ++t) {
+        if (t >= j.T) break;
+        own[t].load(static_cast<const __nv_bfloat16*>(j.x) + static_cast<size_t>(t) * j.K,
+                    (step0 + x_step) * (kStepK / 8) + lane, j.K);
+      }
     };
     auto split_own = [&]() {
       const int blk = lane / 16, c8 = lane % 16;
       uint8_t* to = smem + x_slot * S::kStageBytes + kCodeBytes + blk * S::kXBytes;
       float* side = reinterpret_cast<float*>(sides + side_slot * S::kSideBytes) + blk * (4 / PG + 1) * NT;
-      float sum, factor;
-      split_columns(own, 4 * PG, to + x_chunk(0, c8), x_piece_bytes(NT), sum, factor);
-      if (c8 % (4 * PG) == 0) side[c8 / (4 * PG) * NT] = sum;
-      if (c8 == 0) side[4 / PG * NT] = factor;
+#pragma unroll
+      for (int t = 0; t < (OX ? NT : 1); ++t) {
+        if (t >= j.T) break;
+        float sum, factor;
+        split_columns(own[t], 4 * PG, to + x_chunk(t, c8), x_piece_bytes(NT), sum, factor);
+        if (c8 % (4 * PG) == 0) side[c8 / (4 * PG) * NT + t] = sum;
+        if (c8 == 0) side[4 / PG * NT + t] = factor;
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_full[x_slot]);
@@ -913,15 +922,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One token is split where it is used: no kernel before, no scratch.  (2048 x 2048: 5.2
-// against 5.9 us, and a launch of the host's less; 8192 x 57344 the same.  With two tokens
-// the copying warp falls behind, 50 against 46 us there.)
-bool own_x(int T) { return T == 1; }
-
-// Thread blocks that split K, a cluster: of the powers of two that run at once, the one
-// that leaves the busiest SM the fewest stages, the largest of equal ones.  (Up to 16, not
-// 8: 1027 rows of 7200 columns 7.4 against 8.1 us.  Any number, not powers of two: 14336 x
-// 4096 with 14 blocks 20.2 against 17.1 us.  The smallest of equal ones: 64 tokens at 7168 x 4096 36 against 26 us.)
 int choose_cluster(int K, long long tiles, int per_sm, int num_sms) {
   const int steps = (K + kStepK - 1) / kStepK;
   int best = 1;
@@ -995,39 +995,64 @@ cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaSt
   return checked(cudaLaunchKernelEx(&cfg, w4_kernel<PG, ZP, NT, PS, OX>, map, j), "kernel launch");
 }
 
-template <int PG, bool ZP>
-cudaError_t launch_tokens(const CUtensorMap& map, const W4Job& job, int nt, int num_sms,
-                          cudaStream_t st) {
-  W4Job j = job;
-  const int rows = j.mode == kGateUp ? kRows / 2 : kRows;
-  j.row_tiles = (j.n_rows - 1) / rows + 1;
-  const long long tiles = static_cast<long long>(j.row_tiles) * j.n_blocks;
-  // Up to eight tokens: four blocks an SM, or three, with more registers and a stage more,
-  // where those hold all jobs.  (8192 x 57344, 448 jobs: 44.5 against 45.3 us; 4096 x 28672
-  // in pairs, 448 blocks that need not fit three an SM: 16.8 against 16.0.)
-  if (nt == 8) {
-    j.cluster = choose_cluster(j.K, tiles, 4, num_sms);
-    const bool own = j.mode == kMatvec && own_x(j.T);
-    if (blocks_per_sm(tiles, j.cluster, num_sms) <= 3)
-      return own ? launch<PG, ZP, 8, 3, true>(map, j, num_sms, st)
-                 : launch<PG, ZP, 8, 3>(map, j, num_sms, st);
-    return own ? launch<PG, ZP, 8, 4, true>(map, j, num_sms, st)
-               : launch<PG, ZP, 8, 4>(map, j, num_sms, st);
-  }
-  j.cluster = choose_cluster(j.K, tiles, nt == 16 ? 3 : 2, num_sms);
-  if (nt == 16) return launch<PG, ZP, 16, 3>(map, j, num_sms, st);
-  return launch<PG, ZP, 32, 2>(map, j, num_sms, st);
+struct Plan {
+  int nt, row_tiles, n_blocks, cluster, per_sm;
+  bool own_x;
+};
+
+// How a product runs: tokens of a block, thread blocks of a cluster and of an SM, and
+// who splits x.
+//
+// Up to eight tokens: four blocks an SM, or three, with more registers and a stage more,
+// where those hold all jobs.  (8192 x 57344, 448 jobs: 44.5 against 45.3 us; 4096 x 28672
+// in pairs, 448 blocks that need not fit three an SM: 16.8 against 16.0.)
+//
+// x of a single token, and of few if a thread block has few stages, is split where it is
+// used: no kernel before, no scratch.  (On the device, against a kernel before: one token
+// 2048 x 2048 5.2 to 5.9 us, 8192 x 57344 the same; 5 tokens of 7200 columns, two stages
+// a block, 7.9 to 7.5, and a launch of the host's less; but two tokens at 8192 x 57344 50
+// to 46, as the copying warp falls behind.)
+Plan plan(int mode, int K, int n_rows, int n_blocks, int T, int nt, int num_sms) {
+  Plan p{};
+  p.nt = nt;
+  const int rows = mode == kGateUp ? kRows / 2 : kRows;
+  p.row_tiles = (n_rows - 1) / rows + 1;
+  p.n_blocks = n_blocks;
+  const long long tiles = static_cast<long long>(p.row_tiles) * n_blocks;
+  p.per_sm = nt == 8 ? 4 : nt == 16 ? 3 : 2;
+  p.cluster = choose_cluster(K, tiles, p.per_sm, num_sms);
+  if (nt == 8 && blocks_per_sm(tiles, p.cluster, num_sms) <= 3) p.per_sm = 3;
+  const long long slots = static_cast<long long>(p.per_sm) * num_sms;
+  const int steps = ((K + kStepK - 1) / kStepK + p.cluster - 1) / p.cluster;
+  p.own_x = mode == kMatvec && nt == 8 &&
+            (T == 1 || T * steps * ((tiles * p.cluster + slots - 1) / slots) <= 16);
+  return p;
 }
 
-cudaError_t launch_job(const CUtensorMap& map, int group, const W4Job& j, int nt, int num_sms,
-                       cudaStream_t st) {
+template <int PG, bool ZP>
+cudaError_t launch_planned(const CUtensorMap& map, const W4Job& j, const Plan& p, int num_sms,
+                           cudaStream_t st) {
+  if (p.nt == 32) return launch<PG, ZP, 32, 2>(map, j, num_sms, st);
+  if (p.nt == 16) return launch<PG, ZP, 16, 3>(map, j, num_sms, st);
+  if (p.per_sm == 3)
+    return p.own_x ? launch<PG, ZP, 8, 3, true>(map, j, num_sms, st)
+                   : launch<PG, ZP, 8, 3>(map, j, num_sms, st);
+  return p.own_x ? launch<PG, ZP, 8, 4, true>(map, j, num_sms, st)
+                 : launch<PG, ZP, 8, 4>(map, j, num_sms, st);
+}
+
+cudaError_t launch_job(const CUtensorMap& map, int group, const W4Job& job, const Plan& p,
+                       int num_sms, cudaStream_t st) {
+  W4Job j = job;
+  j.row_tiles = p.row_tiles;
+  j.cluster = p.cluster;
   if (j.zeros != nullptr)
-    return group == 32   ? launch_tokens<1, true>(map, j, nt, num_sms, st)
-           : group == 64 ? launch_tokens<2, true>(map, j, nt, num_sms, st)
-                         : launch_tokens<4, true>(map, j, nt, num_sms, st);
-  return group == 32   ? launch_tokens<1, false>(map, j, nt, num_sms, st)
-         : group == 64 ? launch_tokens<2, false>(map, j, nt, num_sms, st)
-                       : launch_tokens<4, false>(map, j, nt, num_sms, st);
+    return group == 32   ? launch_planned<1, true>(map, j, p, num_sms, st)
+           : group == 64 ? launch_planned<2, true>(map, j, p, num_sms, st)
+                         : launch_planned<4, true>(map, j, p, num_sms, st);
+  return group == 32   ? launch_planned<1, false>(map, j, p, num_sms, st)
+         : group == 64 ? launch_planned<2, false>(map, j, p, num_sms, st)
+                       : launch_planned<4, false>(map, j, p, num_sms, st);
 }
 
 void set_weight(W4Job& j, const W4View& w) {
@@ -1059,7 +1084,7 @@ bool w4_front_fits(int T, int E, int k) {
 
 size_t w4_matvec_scratch(int T, int K) {
   const int nt = w4_block_rows(T);
-  return own_x(T) ? 0 : w4_split_bytes((T + nt - 1) / nt, nt, K, 32);  // the most of any group
+  return T == 1 ? 0 : w4_split_bytes((T + nt - 1) / nt, nt, K, 32);  // the most of any group
 }
 
 size_t w4_split_bytes(long long blocks, int nt, int K, int group) {
@@ -1096,11 +1121,12 @@ cudaError_t launch_w4_matvec(const CUtensorMap& map, const __nv_bfloat16* x, int
   j.T = T;
   j.out = out;
   j.out_fp32 = out_fp32 ? 1 : 0;
-  if (own_x(T)) return launch_job(map, w.group, j, nt, num_sms, st);
+  const Plan how = plan(kMatvec, K, N, j.n_blocks, T, nt, num_sms);
+  if (how.own_x) return launch_job(map, w.group, j, how, num_sms, st);
   const cudaError_t e =
       launch_split(x, T, K, j.n_blocks, nt, w.group, scratch, nullptr, nullptr, 0, 1, st);
   if (e != cudaSuccess) return e;
-  return launch_job(map, w.group, j, nt, num_sms, st);
+  return launch_job(map, w.group, j, how, num_sms, st);
 }
 
 cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
@@ -1139,7 +1165,8 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
                      j.P, p.k, st);
   }
   j.lists_new = w4_front_fits(p.T, p.E, p.k) ? 1 : 0;
-  if (e == cudaSuccess) e = launch_job(map13, p.w13.group, j, nt, num_sms, st);
+  if (e == cudaSuccess) e = launch_job(map13, p.w13.group, j,
+                   plan(kGateUp, p.H, p.I, j.n_blocks, p.T, nt, num_sms), num_sms, st);
   j.lists_new = 0;
   if (e == cudaSuccess)
     e = launch_split(p.h, 0, p.I, j.n_blocks, nt, p.w2.group, p.hq, p.sorted_ids, p.num_padded,
@@ -1152,7 +1179,8 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   j.xq = p.hq;
   j.x = p.h;
   j.out = p.y;
-  e = launch_job(map2, p.w2.group, j, nt, num_sms, st);
+  e = launch_job(map2, p.w2.group, j, plan(kDown, p.I, p.H, j.n_blocks, p.T, nt, num_sms), num_sms,
+                 st);
   if (e != cudaSuccess) return e;
   const long long n = static_cast<long long>(p.T) * (p.H / 4);
   return launch_pdl(w4_combine_kernel,

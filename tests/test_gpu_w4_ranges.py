@@ -158,3 +158,29 @@ def test_layer_ties_go_to_the_lower_expert(gpu_lib, T, E, k):
     gpu_lib.moe_w4_forward(x.cuda(), logits.cuda(), tensor(gpu_lib, p13, 32),
                            tensor(gpu_lib, p2, 32), k, topk_ids_out=ids)
     assert torch.equal(ids.cpu(), torch.arange(k, dtype=torch.int32).expand(T, k))
+
+
+def test_matvec_scratch_of_its_own_on_each_stream(gpu_lib):
+    """Calls with one weight on two streams at a time, and in a graph replayed beside calls
+    of another size, do not disturb one another."""
+    K, N = 4096, 3000
+    parts = ref.make_w4((N, K), 128, "bf16", True, seed=51)
+    w = tensor(gpu_lib, parts, 128)
+    xs = [draw_x(T, K, seed=T).cuda() for T in (12, 40)]
+    want = [gpu_lib.moe_w4_matvec(x, w) for x in xs]
+    graph, y = torch.cuda.CUDAGraph(), torch.empty_like(want[0])
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        for _ in range(20):
+            gpu_lib.moe_w4_matvec(xs[0], w, out=y)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(gpu_lib.moe_w4_matvec(xs[i], w))
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i]) for i in range(2) for g in got[i])
+    assert torch.equal(y, want[0])
