@@ -315,7 +315,9 @@ typedef struct {
 /*
  * Matrix-vector products with 4-bit weights, for a few tokens:
  *   out[t][n] = sum_k x[t][k] * value[n][k],
- * products exact, sums in fp32, one rounding when out is bf16.
+ * products exact (of the largest |x| of 256 columns, what lies 2^-31 below may be
+ * dropped), sums in fp32, one rounding when out is bf16.  A sum that infinities or NaN of
+ * x or the scales enter is what its terms give one by one; others are not touched by them.
  *   x    bf16 [T, K]
  *   w    [N, K] (not NULL)
  *   out  bf16 or fp32 [T, N] (out_dtype)
@@ -323,8 +325,10 @@ typedef struct {
  * (MOE_ERR_UNSUPPORTED otherwise), T < 2^20, K <= 2^20, T*K and T*N < 2^31
  * (MOE_ERR_UNSUPPORTED).
  * `scratch` is a caller buffer of at least moe_w4_matvec_scratch_size(T, K) bytes,
- * 16-byte aligned, that no other call in flight uses.  Results do not depend on
- * anything but the arguments (no atomics).
+ * 16-byte aligned, that no other call in flight uses; it may be NULL where that is 0
+ * (one token).  One or two launches.  Results do not depend on anything but the
+ * arguments.  Waits in the kernel are limited: should a copy never arrive, the rows that
+ * miss it are NaN.
  */
 size_t moe_w4_matvec_scratch_size(int T, int K);
 moe_status_t moe_w4_matvec(const void* x, int T, int K, int N, const moe_w4_tensor* w, void* out,
@@ -354,13 +358,16 @@ int moe_w4_launch_count(int T, int H, int I, int E, int top_k);
 /*
  * The MoE layer of moe_fused_forward with 4-bit expert weights, for a few
  * tokens: the same router, h = SiLU(gate) * up and combine; no activation
- * quantisation.  Any T works; it is built for decode batches, where reading
- * the touched experts' codes bounds the call.
+ * quantisation (x as it is; h from fp32, of which the product uses 11 significant bits).
+ * Any T works; it is built for decode batches, where reading the touched experts' codes
+ * bounds the call.
  * Requires 1 <= top_k <= E <= 1024, H % 32 == 0 and I % 32 == 0
+ * and T*top_k*H, T*top_k*I < 2^36, T*top_k < 2^30, H < 2^19, I < 2^18
  * (MOE_ERR_UNSUPPORTED otherwise), T >= 0, a device of compute capability
  * 10.3, workspace of moe_w4_workspace_size() bytes (256-byte aligned) that no
  * other in-flight call uses.  T == 0 returns MOE_OK and enqueues nothing (no
  * output is written).  Results do not depend on anything but the arguments.
+ * moe_check_status() tells of a wait that gave up (its rows are NaN then).
  */
 moe_status_t moe_w4_forward(const moe_w4_args* args, void* workspace, size_t workspace_bytes,
                             moe_stream_t stream);

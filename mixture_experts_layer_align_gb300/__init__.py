@@ -511,7 +511,8 @@ def moe_w4_matvec(x, w: W4Tensor, out=None, out_dtype=None, scratch=None, stream
     """Matrix-vector products with 4-bit weights, for a few tokens: out = x w^T.
     x: bf16 [T, K]; w: W4Tensor [N, K]; out: bf16 or fp32 [T, N] (allocated, of
     `out_dtype`, bf16 by default, when not given); scratch: uint8,
-    moe_w4_matvec_scratch_size(T, K) bytes (allocated when not given).  Returns out."""
+    moe_w4_matvec_scratch_size(T, K) bytes (when not given, one that the weight keeps for
+    the current stream, or one for this call).  Returns out."""
     import torch
     _require(x, torch.bfloat16, "x")
     if len(w.shape) != 2 or x.dim() != 2 or x.shape[1] != w.shape[1]:
