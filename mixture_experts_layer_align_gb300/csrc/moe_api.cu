@@ -865,8 +865,10 @@ size_t moe_w4_workspace_size(int T, int H, int I, int E, int top_k) {
 
 int moe_w4_launch_count(int T, int H, int I, int E, int top_k) {
   if (!w4_sizes_ok(T, H, I, E, top_k) || !w4_sizes_supported(T, H, I, top_k)) return -1;
-  // router, alignment and split, or a kernel for each; gate/up, split, down, combine
-  return T == 0 ? 0 : w4_front_fits(T, E, top_k) ? 5 : 7;
+  // router, alignment and split of x (for few pairs one kernel); gate/up; split of h (a
+  // single token's by the next); down; combine
+  if (T == 0) return 0;
+  return (w4_front_fits(T, E, top_k) ? 1 : 3) + (T == 1 ? 3 : 4);
 }
 
 moe_status_t moe_w4_forward(const moe_w4_args* a, void* workspace, size_t workspace_bytes,

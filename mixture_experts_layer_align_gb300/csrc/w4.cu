@@ -376,7 +376,7 @@ struct W4Job {
   const uint8_t* xq;        // x (down: h), split: an XLayout for each block of tokens
   const void* x;            // tokens, bf16 (down: h by pair, fp32)
   int T;
-  void* out;     // matvec: [T][N]; gate/up: h bf16 [pair][I]; down: y fp32 [pair][H]
+  void* out;     // matvec: [T][N]; gate/up: h fp32 [pair][I]; down: y fp32 [pair][H]
   int out_fp32;
   int cluster;   // thread blocks that split K
   int stages;    // of codes
@@ -390,7 +390,7 @@ struct W4Job {
   int* err;      // status word, or null
 };
 
-template <int PG, int NT, int PS>
+template <int PG, int NT>
 struct W4Shape {
   static constexpr int kN = NT < 16 ? 16 : NT;  // MMA N (16 at least with 128 rows)
   static constexpr int kTmem = NT <= 16 ? 128 : 256;  // columns of tensor memory
@@ -438,13 +438,14 @@ __device__ __noinline__ float w4_row_plain(const W4Job& j, int group, size_t gro
 }
 
 // PG: 32-column pieces of a group (1, 2, 4).  NT: tokens of a block at most.  PS:
-// thread blocks of an SM.  OX: eight tokens at most, which the copying warp splits itself.
+// thread blocks of an SM.  OX: the copying warp splits
+// x itself, eight tokens at most (layer: h of a single one).
 // A cluster (of one block, where there are more jobs than clusters) takes every
 // gridDim.x / j.cluster-th job: a tile of rows for a block of tokens.
 template <int PG, bool ZP, int NT, int PS, bool OX>
 __global__ void __launch_bounds__(kThreads, PS)
     w4_kernel(const __grid_constant__ CUtensorMap map, const W4Job j) {
-  using S = W4Shape<PG, NT, PS>;
+  using S = W4Shape<PG, NT>;
   constexpr int kMmaThreads = kRowThreads + 32;  // at the barriers of A
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kMaxStages];   // a stage's codes and x are there
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, PS)
   // The kernel before splits x, and waited itself for those before it: the weights, and
   // the lists where it does not write them, are older than it and are read before
   // pdl_wait().
-  if (OX || j.lists_new) pdl_wait();
+  if (OX ? !layer : j.lists_new) pdl_wait();
   const int job0 = static_cast<int>(blockIdx.x) / CS, job_step = static_cast<int>(gridDim.x) / CS;
   // (the first job's expert with the number of jobs; it is one's number if there is one)
   const int expert0 = layer ? __ldcg(j.block_expert + job0 / j.row_tiles) : 0;
@@ -575,7 +576,14 @@ __global__ void __launch_bounds__(kThreads, PS)
     const uint8_t* xq = j.xq + x_job / j.row_tiles * lay.bytes();
     // OX: the 256 columns to come of each token, on their way
     Columns<__nv_bfloat16> own[OX ? NT : 1];
+    Columns<float> own_h;
     auto fetch_own = [&]() {
+      if (layer) {
+        const size_t pair = __ldcg(j.sorted_ids + x_job / j.row_tiles * NT);
+        own_h.load(static_cast<const float*>(j.x) + pair * j.K,
+                   (step0 + x_step) * (kStepK / 8) + lane, j.K);
+        return;
+      }
 #pragma unroll
       for (int t = 0; t < (OX ? NT : 1); ++t) {
         if (t >= j.T) break;
@@ -591,7 +599,8 @@ __global__ void __launch_bounds__(kThreads, PS)
       for (int t = 0; t < (OX ? NT : 1); ++t) {
         if (t >= j.T) break;
         float sum, factor;
-        split_columns(own[t], 4 * PG, to + x_chunk(t, c8), x_piece_bytes(NT), sum, factor);
+        if (layer) split_columns(own_h, 4 * PG, to + x_chunk(t, c8), x_piece_bytes(NT), sum, factor);
+        else split_columns(own[t], 4 * PG, to + x_chunk(t, c8), x_piece_bytes(NT), sum, factor);
         if (c8 % (4 * PG) == 0) side[c8 / (4 * PG) * NT + t] = sum;
         if (c8 == 0) side[4 / PG * NT + t] = factor;
       }
@@ -599,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, PS)
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_full[x_slot]);
     };
-    if (OX) fetch_own();
     auto issue_x = [&]() {
       if (x_job >= n_jobs) return;
       if (OX) {
@@ -632,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, PS)
     pdl_wait();
     pdl_trigger();
     fence_proxy_async_global();  // x was written by ordinary stores
+    if (OX) fetch_own();
     for (int i = 0; i < j.stages; ++i) issue_x();
     int slot = 0, phase = 0;
     while (c_job < n_jobs) {
@@ -964,7 +973,7 @@ cudaError_t allow(const void* kernel, std::atomic<uint64_t>& done) {
 
 template <int PG, bool ZP, int NT, int PS, bool OX = false>
 cudaError_t launch(const CUtensorMap& map, const W4Job& job, int num_sms, cudaStream_t st) {
-  using S = W4Shape<PG, NT, PS>;
+  using S = W4Shape<PG, NT>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow(reinterpret_cast<const void*>(w4_kernel<PG, ZP, NT, PS, OX>), done);
   if (e != cudaSuccess) return e;
@@ -1011,7 +1020,7 @@ struct Plan {
 // used: no kernel before, no scratch.  (On the device, against a kernel before: one token
 // 2048 x 2048 5.2 to 5.9 us, 8192 x 57344 the same; 5 tokens of 7200 columns, two stages
 // a block, 7.9 to 7.5, and a launch of the host's less; but two tokens at 8192 x 57344 50
-// to 46, as the copying warp falls behind.)
+// to 46, as the copying warp falls behind.)  A layer's single token likewise for h.
 Plan plan(int mode, int K, int n_rows, int n_blocks, int T, int nt, int num_sms) {
   Plan p{};
   p.nt = nt;
@@ -1024,8 +1033,10 @@ Plan plan(int mode, int K, int n_rows, int n_blocks, int T, int nt, int num_sms)
   if (nt == 8 && blocks_per_sm(tiles, p.cluster, num_sms) <= 3) p.per_sm = 3;
   const long long slots = static_cast<long long>(p.per_sm) * num_sms;
   const int steps = ((K + kStepK - 1) / kStepK + p.cluster - 1) / p.cluster;
-  p.own_x = mode == kMatvec && nt == 8 &&
-            (T == 1 || T * steps * ((tiles * p.cluster + slots - 1) / slots) <= 16);
+  if (mode == kMatvec)
+    p.own_x = nt == 8 &&
+              (T == 1 || T * steps * ((tiles * p.cluster + slots - 1) / slots) <= 16);
+  if (mode == kDown) p.own_x = T == 1;  // (the front kernel splits x along the way)
   return p;
 }
 
@@ -1168,7 +1179,8 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   if (e == cudaSuccess) e = launch_job(map13, p.w13.group, j,
                    plan(kGateUp, p.H, p.I, j.n_blocks, p.T, nt, num_sms), num_sms, st);
   j.lists_new = 0;
-  if (e == cudaSuccess)
+  const Plan down = plan(kDown, p.I, p.H, j.n_blocks, p.T, nt, num_sms);
+  if (e == cudaSuccess && !down.own_x)
     e = launch_split(p.h, 0, p.I, j.n_blocks, nt, p.w2.group, p.hq, p.sorted_ids, p.num_padded,
                      j.P, 1, st);
   if (e != cudaSuccess) return e;
@@ -1179,8 +1191,7 @@ cudaError_t launch_w4_layer(const CUtensorMap& map13, const CUtensorMap& map2,
   j.xq = p.hq;
   j.x = p.h;
   j.out = p.y;
-  e = launch_job(map2, p.w2.group, j, plan(kDown, p.I, p.H, j.n_blocks, p.T, nt, num_sms), num_sms,
-                 st);
+  e = launch_job(map2, p.w2.group, j, down, num_sms, st);
   if (e != cudaSuccess) return e;
   const long long n = static_cast<long long>(p.T) * (p.H / 4);
   return launch_pdl(w4_combine_kernel,
