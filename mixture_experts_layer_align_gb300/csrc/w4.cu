@@ -19,8 +19,8 @@
 // (mma.sync from registers, a bf16 multiply-add for each pair of codes, took 24 us for a
 // token at 4096 x 28672, this 16; bf16 codes in tensor memory twice the stores.)
 //
-// x is split once for a call, by a kernel before, for a single token by the kernel that
-// uses it.  A thread block owns 128 weight rows for a block of 8, 16 or 32 tokens at a
+// x is split once for a call, by a kernel before, for a single token (and few of them, if
+// a block has few stages) by the kernel that uses it.  A thread block owns 128 weight rows for a block of 8, 16 or 32 tokens at a
 // time; it stays for all its jobs, so that copies run on from one to the next (a block
 // for each job, most of them empty for a layer's upper bound of them: 185 against 120 us,
 // gate/up of 32 tokens on 256 experts).  Where there are fewer jobs than blocks that run
@@ -30,9 +30,9 @@
 // the codes of a unit into tensor memory (A, 128 rows) and, while its MMAs run, scale the
 // sums of the unit before in fp32.
 //
-// Measured (device, one call of many in a row): one token at 8192 x 57344 44 us, 80 % of
-// the bytes' time; at 4096 x 28672 16; 2048 x 2048 5.1.  32 tokens at 8192 x 57344 75,
-// where adding up the sums takes as long as the codes.
+// Measured (device, one call of many in a row): one token at 8192 x 57344 44.6 to 46 us,
+// where the bytes take 35.6; at 4096 x 28672 15; 2048 x 2048 5.1.  16 tokens at 8192 x
+// 57344 49; 32 tokens 75, in two rounds of thread blocks.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
